@@ -256,6 +256,90 @@ typedef struct {
 
 int moe_lora_workspace_layout(const moe_lora_dims *d, int32_t topk, moe_lora_layout_info *out);
 
+/* Expert choice of a router whose scores, weights and groups differ from moe_lora_forward's own
+ * routing (page "vLLM MoE LoRA SageMaker Bedrock", section "Entendendo os Modelos MoE": the
+ * router sends each token to its most relevant experts). Per token, over the experts whose logit
+ * is finite (others, and with a bias those whose bias is not finite, are never chosen):
+ *   score    s_e = softmax over those experts, or 1 / (1 + exp(-logit_e));
+ *   choice   c_e = s_e + bias_e. Without a bias the experts rank by their logits, which order
+ *            them as the scores do (by the scores where groups are ranked by a sum of two);
+ *   groups   n_groups runs of n_experts / n_groups consecutive experts. A group ranks by its
+ *            largest choice value, or by the sum of its two largest (of the one, where a group has
+ *            one expert to choose); the topk_groups best keep their experts, ties to the lower
+ *            group;
+ *   slots    the topk largest choice values in falling order, ties to the lower expert id. A token
+ *            with fewer experts to choose has expert -1 and weight 0 in the slots left;
+ *   weight   scale * s_e, or with renormalize scale * s_e / (sum of the chosen s). The bias steers
+ *            the choice and is no part of the weight.
+ * Choice values are computed in double precision and told apart at 2^-42 of their size. */
+#define MOELORA_SCORE_SOFTMAX 0
+#define MOELORA_SCORE_SIGMOID 1
+#define MOELORA_GROUP_MAX 0
+#define MOELORA_GROUP_TOP2 1
+typedef struct {
+  int32_t T, n_experts, topk; /* T >= 0; n_experts in [1, 1024]; topk in [1, min(n_experts, 16)] */
+  int32_t scoring;            /* MOELORA_SCORE_* */
+  int32_t n_groups;           /* divides n_experts, at most 64 */
+  int32_t topk_groups;        /* in [1, n_groups]; topk <= topk_groups * n_experts / n_groups */
+  int32_t group_score;        /* MOELORA_GROUP_* */
+  int32_t renormalize;        /* 0 or 1 */
+  float scale;                /* finite */
+  int64_t logits_stride;      /* floats between two tokens' logits, >= n_experts */
+} moe_lora_router;
+
+/* Chooses experts by `r` (above). logits f32 [T] rows of n_experts, bias f32 [n_experts] or NULL,
+ * token_mask uint8 [T] or NULL (0: a row of padding, whose logits are not read and whose slots all
+ * stay empty), topk_ids int32 [T][topk], topk_w f32 [T][topk], token_flags int32 [T] or NULL (1
+ * where a logit of the token was not finite). Device pointers, caller-owned, aligned to their
+ * elements; no workspace. topk_ids and topk_w go into moe_lora_forward_topk. Asynchronous on
+ * `stream`. Errors: MOELORA_EINVAL_DIMS for a field out of the ranges above, MOELORA_ENULL,
+ * MOELORA_EALIGN, MOELORA_EDEVICE, MOELORA_EHIP. With T = 0 nothing is enqueued. */
+int moe_lora_route(const float *logits, const float *bias, const uint8_t *token_mask,
+                   const moe_lora_router *r, int32_t *topk_ids, float *topk_w,
+                   int32_t *token_flags, void *stream);
+
+/* Dense projection with its epilogue (page "vLLM MoE LoRA SageMaker Bedrock", section "O Papel da
+ * Multi-LoRA": the frozen product xW that moe_lora_sgmv adds a batch's adapters to; section
+ * "Entendendo os Modelos MoE": gate_up and down of an expert that every token takes):
+ *   y[t][n] = act(w_scale[n] * sum_k x[t][k] W[n][k] + bias[n]) + residual[t][n]
+ * with the sums, the scale, the bias, the activation and the residual in fp32 and one rounding to
+ * bf16. Activations: none; relu; silu v / (1 + e^-v); gelu v Phi(v); its tanh form
+ * v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3))); SwiGLU, for which W (w_scale, bias) has
+ * 2 out_features rows, gate then up, and act = silu(gate) * up. */
+#define MOELORA_ACT_NONE 0
+#define MOELORA_ACT_RELU 1
+#define MOELORA_ACT_SILU 2
+#define MOELORA_ACT_GELU 3
+#define MOELORA_ACT_GELU_TANH 4
+#define MOELORA_ACT_SWIGLU 5
+#define MOELORA_W_BF16 0
+#define MOELORA_W_E4M3 1
+typedef struct {
+  int32_t T, in_features, out_features; /* T >= 0; in_features a positive multiple of 8 (E4M3: of
+                                           16); out_features >= 1 */
+  int32_t act;    /* MOELORA_ACT_* */
+  int32_t w_type; /* MOELORA_W_BF16, or MOELORA_W_E4M3: OCP E4M3 codes with one scale per row, as
+                     in moe_lora_forward_fp8 */
+  /* elements between two rows, at least a row's length and under 2^22: x and W rows a multiple of
+   * 16 bytes; y and the residual (ignored when NULL) any */
+  int64_t x_stride, w_stride, y_stride, residual_stride;
+} moe_lora_linear_dims;
+
+/* Bytes of device workspace moe_lora_linear needs for these sizes: the sums of a split reduction
+ * where the output tiles alone would not fill the GPU, 0 where it takes none (and for sizes that
+ * are not supported). 256-byte aligned, no initialisation needed. Host-only. */
+size_t moe_lora_linear_workspace_size(const moe_lora_linear_dims *d);
+
+/* The projection above. x bf16, W bf16 or E4M3 codes (both 16-byte aligned), w_scale f32 (E4M3
+ * only, else NULL), bias bf16 or NULL, residual bf16 or NULL, y bf16 (aligned to their elements).
+ * y may be the residual itself (the same pointer and stride), and no other overlap of y with an
+ * input is allowed. workspace may be NULL where its size is 0. Results do not depend on timing:
+ * the same call gives the same bits. Asynchronous on `stream`; allocates nothing. With T = 0
+ * nothing is enqueued and no pointer is inspected. */
+int moe_lora_linear(const void *x, const void *W, const float *w_scale, const void *bias,
+                    const void *residual, const moe_lora_linear_dims *d, void *y, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
 /* Text for a return code (the MOELORA_E* codes above; no page defines them). Never NULL; the
  * string is static and owned by the library. */
 const char *moe_lora_strerror(int code);

@@ -23,6 +23,7 @@ EXPORTS = ("moe_lora_workspace_size", "moe_lora_forward", "moe_lora_forward_time
            "moe_lora_sorted_capacity", "moe_lora_route_align", "moe_lora_strerror",
            "moe_lora_debug_status", "moe_lora_sgmv_workspace_size", "moe_lora_sgmv",
            "moe_lora_router_logits", "moe_lora_forward_routed", "moe_lora_workspace_layout",
+           "moe_lora_route", "moe_lora_linear", "moe_lora_linear_workspace_size",
            "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
 N_STAGES = 7
 STAGES = ("route", "align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
@@ -48,6 +49,21 @@ class LayoutInfo(ctypes.Structure):
 class SgmvDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "in_features", "out_features", "n_adapters", "rank")]
 
+
+class Router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "n_experts", "topk", "scoring", "n_groups", "topk_groups",
+                                              "group_score", "renormalize")] + [
+        ("scale", ctypes.c_float), ("logits_stride", ctypes.c_int64)]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "in_features", "out_features", "act", "w_type")] + [
+        (n, ctypes.c_int64) for n in ("x_stride", "w_stride", "y_stride", "residual_stride")]
+
+
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 
 _lib = None
 
@@ -92,6 +108,12 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_route_align.restype = ctypes.c_int
         L.moe_lora_workspace_layout.argtypes = [D, i32, ctypes.POINTER(LayoutInfo)]
         L.moe_lora_workspace_layout.restype = ctypes.c_int
+        L.moe_lora_route.argtypes = [P, P, P, ctypes.POINTER(Router), P, P, P, P]
+        L.moe_lora_route.restype = ctypes.c_int
+        L.moe_lora_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDims)]
+        L.moe_lora_linear_workspace_size.restype = ctypes.c_size_t
+        L.moe_lora_linear.argtypes = [P, P, P, P, P, ctypes.POINTER(LinearDims), P, P, ctypes.c_size_t, P]
+        L.moe_lora_linear.restype = ctypes.c_int
         L.moe_lora_strerror.argtypes = [ctypes.c_int]
         L.moe_lora_strerror.restype = ctypes.c_char_p
         L.moe_lora_debug_status.argtypes = [P, ctypes.c_size_t, P, ctypes.POINTER(ctypes.c_uint32)]
@@ -318,6 +340,120 @@ def sgmv(x, A, B, adapter_ids, y, workspace=None) -> torch.Tensor:
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check(lib().moe_lora_sgmv(_ptr(x), _ptr(A), _ptr(B), _ptr(adapter_ids), ctypes.byref(d), _ptr(y),
                                _ptr(workspace), workspace.numel(), _stream(x.device)), "moe_lora_sgmv")
+    return y
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Checks a matrix whose rows may lie apart (their elements adjacent); its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    row, col = t.stride()
+    if shape[1] > 1 and col != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    if shape[0] <= 1:  # (the stride of a single row means nothing)
+        return max(row, shape[1])
+    if row < shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return row
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+          group_score: str = "max", renormalize: bool = True, scale: float = 1.0, token_mask=None,
+          topk_ids=None, topk_w=None, token_flags=None):
+    """Expert choice of a router (moe_lora_route): (topk_ids [T][topk] int32, topk_w [T][topk]
+    float32) of logits [T][E] float32 (rows may lie apart), the arguments of forward_topk.
+
+    scoring: "softmax" over the experts or "sigmoid"; bias [E] float32 steers the choice only;
+    n_groups, topk_groups, group_score ("max" or "top2"): only the best groups' experts are
+    chosen from; renormalize: weights over the sum of the chosen; token_mask [T] bool: False for
+    rows of padding. Empty slots hold expert -1 and weight 0. token_flags [T] int32, when given,
+    receives 1 where a token's logits were not all finite."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [T][E] tensor")
+    T, E = logits.shape
+    stride = _rows(logits, "logits", torch.float32, (T, E))
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring must be one of {sorted(SCORINGS)}")
+    if group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}")
+    if bias is not None:
+        _expect(bias, "bias", torch.float32, (E,))
+    if token_mask is not None:
+        _expect(token_mask, "token_mask", torch.bool, (T,))
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
+    else:
+        _expect(topk_ids, "topk_ids", torch.int32, (T, topk))
+    if topk_w is None:
+        topk_w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
+    else:
+        _expect(topk_w, "topk_w", torch.float32, (T, topk))
+    if token_flags is not None:
+        _expect(token_flags, "token_flags", torch.int32, (T,))
+    _same_device(dev, bias=bias, token_mask=token_mask, topk_ids=topk_ids, topk_w=topk_w,
+                 token_flags=token_flags)
+    r = Router(T, E, topk, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score],
+               1 if renormalize else 0, scale, stride)
+    with torch.cuda.device(dev):
+        _check(lib().moe_lora_route(_ptr(logits), _ptr(bias), _ptr(token_mask), ctypes.byref(r),
+                                    _ptr(topk_ids), _ptr(topk_w), _ptr(token_flags), _stream(dev)),
+               "moe_lora_route")
+    return topk_ids, topk_w
+
+
+def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y=None,
+           workspace=None) -> torch.Tensor:
+    """Dense projection y = act(x W^T + bias) + residual (moe_lora_linear), bf16 [T][N].
+
+    x [T][K] bf16; W [N][K] bf16, or uint8 E4M3 codes with w_scale [N] float32; bias [N] and
+    residual [T][N] bf16. act: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu", for which
+    W (w_scale, bias) has 2 N rows, gate then up. Rows of x, W, residual and y may lie apart (x
+    and W rows 16-byte aligned). y may be the residual. sgmv(x, A, B, adapter_ids, y) adds a
+    batch's adapters to a projection without an activation."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("x must be [T][K] and W [N][K]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    T, K = x.shape
+    rows = W.shape[0]
+    if act == "swiglu" and rows % 2:
+        raise ValueError("W of swiglu has gate and up rows: an even number")
+    N = rows // 2 if act == "swiglu" else rows
+    bf = torch.bfloat16
+    xs = _rows(x, "x", bf, (T, K))
+    ws = _rows(W, "W", bf if w_scale is None else torch.uint8, (rows, K))
+    if w_scale is not None:
+        _expect(w_scale, "w_scale", torch.float32, (rows,))
+    if bias is not None:
+        _expect(bias, "bias", bf, (rows,))
+    rs = _rows(residual, "residual", bf, (T, N)) if residual is not None else 0
+    dev = x.device
+    if y is None:
+        y = torch.empty((T, N), dtype=bf, device=dev)
+    ys = _rows(y, "y", bf, (T, N))
+    d = LinearDims(T, K, N, ACTIVATIONS[act], 0 if w_scale is None else 1, xs, ws, ys, rs)
+    L = lib()
+    need = L.moe_lora_linear_workspace_size(ctypes.byref(d))
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _same_device(dev, W=W, w_scale=w_scale, bias=bias, residual=residual, y=y, workspace=workspace)
+    with torch.cuda.device(dev):
+        _check(L.moe_lora_linear(_ptr(x), _ptr(W), _ptr(w_scale), _ptr(bias), _ptr(residual), ctypes.byref(d),
+                                 _ptr(y), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                 _stream(dev)), "moe_lora_linear")
     return y
 
 

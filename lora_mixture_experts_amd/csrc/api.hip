@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "common.h"
+#include "host.h"
 #include "kernels.h"
 #include "moelora.h"
 
@@ -18,7 +19,6 @@ constexpr int kMaxBM = 256;      // largest row block any GEMM path uses
 constexpr int kMaxDownSplit = 2;  // K splits of the down GEMM
 constexpr size_t kScratchBytes = (size_t)128 << 20;  // static scratch of the no-alloc entry
 
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t round_up64(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 int validate_dims(const moe_lora_dims* d, int32_t topk) {
@@ -39,21 +39,6 @@ int validate_dims(const moe_lora_dims* d, int32_t topk) {
   // so is one expert's slice of W1 (2I x h, the larger of the two projections)
   if ((int64_t)2 * d->inter * d->hidden * 2 >= ((int64_t)1 << 31)) return MOELORA_EINVAL_DIMS;
   return MOELORA_OK;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-int check_device() {
-  static int known[64];  // 0 unknown, 1 gfx950, -1 other
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return MOELORA_EHIP;
-  if (dev < 0 || dev >= 64) return MOELORA_EDEVICE;
-  if (known[dev] == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MOELORA_EHIP;
-    known[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
-  }
-  return known[dev] == 1 ? MOELORA_OK : MOELORA_EDEVICE;
 }
 
 // Workgroups of the 256-row tiled GEMM resident at once: one per CU, rounded down to the 8 XCDs

@@ -69,6 +69,26 @@ struct SgmvSortArgs {
   int* flags;         // [1]: MOELORA_FLAG_ADAPTER_RANGE when an id is out of range
 };
 
+// Expert choice with scores, bias, groups and weights (moe_lora_route).
+struct RouteScoredArgs {
+  const float* logits;  // [T] rows of E, ld floats apart
+  int64_t ld;
+  const float* bias;          // [E] or nullptr
+  const uint8_t* token_mask;  // [T] or nullptr: 0 for a row of padding
+  int T, k;
+  int G, S;         // groups of S consecutive experts (E = G * S)
+  int topk_groups;  // groups that keep their experts
+  int group_top2;   // a group's score: the sum of its two largest choice values, else the largest
+  int scoring;      // 0 softmax over the experts, 1 sigmoid
+  int by_score;     // choice values are scores (+ bias); 0: the logits rank
+  int renormalize;
+  float scale;
+  int* topk_ids;     // [T][k], -1 for an empty slot
+  float* topk_w;     // [T][k], 0 for an empty slot
+  int* token_flags;  // [T] or nullptr: 1 where a logit of the row was not finite
+  int Gp, vec;       // (launcher) G rounded up to a power of two; rows and groups load 16 bytes
+};
+
 // LoRA shrink z = X A^T for the rows of the sorted layout.
 struct ShrinkArgs {
   const uint16_t* X;  // gather: x [T][K]; otherwise act [cap][K]
@@ -145,6 +165,31 @@ struct SgmvArgs {
   int N, r;
 };
 
+// Dense projection y = act(scale * (x W^T) + bias) + residual (moe_lora_linear). SwiGLU: W holds
+// 2 N rows, gate then up.
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSwiglu = 5 };
+constexpr int kLinearStreamTokens = 64;  // token rows the weight-streaming kernel takes
+struct LinearArgs {
+  const uint16_t* X;    // [T] rows of K bf16, ldx apart
+  const void* W;        // [rows] rows of K bf16, or E4M3 codes when wscale is given, ldw apart
+  const float* wscale;  // [rows] or nullptr
+  const uint16_t* bias; // [rows] bf16 or nullptr
+  const uint16_t* R;    // residual: [T] rows of N bf16, ldr apart, or nullptr
+  uint16_t* Y;          // [T] rows of N bf16, ldy apart
+  int64_t ldx, ldw, ldr, ldy;
+  int T, N, K;
+  int64_t rows;  // weight rows: N, or 2 N for SwiGLU
+  int act;
+  int vec;  // rows of y and of the residual may be accessed 8 bytes at a time
+  // tiled
+  float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
+  int splits, row_tiles, col_tiles;
+};
+struct LinearPlan {
+  bool stream;
+  int bm, bn, splits;
+};
+
 // Tile shape of the LDS-staged GEMM: nw wavefronts of WM x WN each; NST LDS stages of BK k.
 struct TiledConfig {
   int bm, bn, wm, wn;
@@ -164,6 +209,7 @@ struct SkinnyConfig {
 // Host launchers (each defined next to its kernel). They return the launch status.
 hipError_t launch_route(const float* logits, int T, int E, int k, int* topk_ids, float* topk_w,
                         int* tok_flags, hipStream_t stream);
+hipError_t launch_route_scored(RouteScoredArgs a, hipStream_t stream);
 hipError_t launch_align(const AlignArgs& a, size_t dyn_lds, hipStream_t stream);
 hipError_t launch_sgmv_sort(const SgmvSortArgs& a, hipStream_t stream);
 hipError_t launch_router_logits(const uint16_t* x, const uint16_t* W, int T, int K, int E,
@@ -180,6 +226,8 @@ hipError_t launch_skinny(const SkinnyConfig& c, bool gateup, const GemmArgs& a, 
                          hipStream_t stream, bool fp8 = false);
 hipError_t launch_tiled(const TiledConfig& c, bool gateup, const GemmArgs& a, hipStream_t stream,
                         bool fp8 = false);
+hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream);
+hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t stream);
 hipError_t launch_sgmv_expand(const SgmvArgs& a, int max_blocks, hipStream_t stream);
 // D parts: d_parts == nullptr: ksplit parts for every row; else d_parts[(row / part_rows) *
 // part_ncol + col / part_cols] parts (1 to 4) for the tile holding (row, col).
