@@ -2,6 +2,10 @@
 // projection (moe_lora_linear), declared in include/moelora.h. Argument checks and launches.
 #include <algorithm>
 #include <math.h>
+#ifdef TUNE
+#include <stdio.h>
+#include <stdlib.h>
+#endif
 
 #include "common.h"
 #include "host.h"
@@ -53,8 +57,11 @@ int validate_linear(const moe_lora_linear_dims* d, bool residual) {
 LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   LinearPlan p{};
   p.splits = 1;
+  p.nst = 2;
   p.stream = d->T <= kLinearStreamTokens;
+#ifndef TUNE
   if (p.stream) return p;
+#endif
   const int64_t rows = (int64_t)d->out_features * (d->act == MOELORA_ACT_SWIGLU ? 2 : 1);
   auto tiles = [&](int bm, int bn) {
     return (((int64_t)d->T + bm - 1) / bm) * ((rows + bn - 1) / bn);
@@ -65,6 +72,12 @@ LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   const int64_t n = tiles(p.bm, p.bn);
   const int steps = (d->in_features + 63) / 64;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / n, (int64_t)steps / 8, 8}));
+#ifdef TUNE
+  if (const char* e = getenv("LIN")) {
+    int st;
+    if (sscanf(e, "%d,%d,%d,%d,%d", &st, &p.bm, &p.bn, &p.nst, &p.splits) == 5) p.stream = st;
+  }
+#endif
   return p;
 }
 
@@ -148,7 +161,9 @@ int moe_lora_linear(const void* x, const void* W, const float* w_scale, const vo
   a.K = d->in_features;
   a.rows = (int64_t)d->out_features * (d->act == MOELORA_ACT_SWIGLU ? 2 : 1);
   a.act = d->act;
-  a.vec = ((uintptr_t)y & 7u) == 0 && a.ldy % 4 == 0 && ((uintptr_t)residual & 7u) == 0 && a.ldr % 4 == 0;
+  const uint64_t low = (uint64_t)(uintptr_t)y | (uint64_t)(uintptr_t)residual | (uint64_t)(2 * a.ldy) |
+                       (uint64_t)(2 * a.ldr);
+  a.vec = low % 16 == 0 ? 16 : (low % 8 == 0 ? 8 : 2);
   a.part = (float*)workspace;
   a.splits = 1;
   a.row_tiles = a.col_tiles = 0;

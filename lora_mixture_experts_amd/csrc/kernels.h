@@ -180,14 +180,15 @@ struct LinearArgs {
   int T, N, K;
   int64_t rows;  // weight rows: N, or 2 N for SwiGLU
   int act;
-  int vec;  // rows of y and of the residual may be accessed 8 bytes at a time
+  int vec;  // bytes of the largest access that rows of y and of the residual allow: 2, 8 or 16
   // tiled
   float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
   int splits, row_tiles, col_tiles;
 };
 struct LinearPlan {
   bool stream;
-  int bm, bn, splits;
+  int bm, bn, nst;  // tile and LDS stages
+  int splits;       // of the reduction
 };
 
 // Tile shape of the LDS-staged GEMM: nw wavefronts of WM x WN each; NST LDS stages of BK k.

@@ -7,38 +7,66 @@
 
 namespace moelora {
 
-// Activation of one value (SwiGLU takes two: swiglu below). The exponentials of large arguments
-// run into infinity or zero, which gives the activations' limits.
-__device__ __forceinline__ float linear_act(int act, float v) {
+// Activation of C values (SwiGLU takes two of them: swiglu below). The exponentials of large
+// arguments run into infinity or zero, which gives the activations' limits.
+template <int C>
+__device__ __forceinline__ void linear_act(int act, float (&v)[C]) {
   switch (act) {
-    case kActRelu: return v > 0.f || v != v ? v : 0.f;
-    case kActSilu: return v / (1.f + __expf(-v));
-    // x * Phi(x) with Phi(x) = erfc(-x / sqrt 2) / 2: no cancellation for negative x
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678f * v);
-    // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
-    case kActGeluTanh: return v / (1.f + __expf(-1.5957691f * v * (1.f + 0.044715f * v * v)));
-    default: return v;
+    case kActRelu:
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] = v[c] < 0.f ? 0.f : v[c];  // (NaN stays NaN)
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] = v[c] / (1.f + __expf(-v[c]));
+      break;
+    case kActGelu:  // x * Phi(x) with Phi(x) = erfc(-x / sqrt 2) / 2: no cancellation for negative x
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] = 0.5f * v[c] * erfcf(-0.70710678f * v[c]);
+      break;
+    case kActGeluTanh:  // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        v[c] = v[c] / (1.f + __expf(-1.5957691f * v[c] * (1.f + 0.044715f * v[c] * v[c])));
+      break;
+    default:
+      break;
   }
 }
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-// 4 consecutive output columns n.. of token row t: residual, rounding and store. `vec`: rows of y
-// and of the residual may be accessed 8 bytes at a time.
-__device__ __forceinline__ void linear_store4(const LinearArgs& a, int t, int n, f32x4 v) {
+// C (4 or 8) consecutive output columns n.. of token row t: residual, rounding and store, as one
+// access of 2 C bytes where the rows of y and of the residual allow it (a.vec: the largest access
+// in bytes that their strides and addresses do).
+template <int C>
+__device__ __forceinline__ void linear_store(const LinearArgs& a, int t, int n, float (&v)[C]) {
   const int64_t yo = (int64_t)t * a.ldy + n, ro = (int64_t)t * a.ldr + n;
-  if (a.vec && n + 3 < a.N) {
+  if (a.vec >= 2 * C && n + C <= a.N) {
+    uint32_t w[C / 2];
     if (a.R) {
-      const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + ro);
-      v[0] += bf16_lo(r.x);
-      v[1] += bf16_hi(r.x);
-      v[2] += bf16_lo(r.y);
-      v[3] += bf16_hi(r.y);
+      if constexpr (C == 8) {
+        const u32x4 r = *reinterpret_cast<const u32x4*>(a.R + ro);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = r[i];
+      } else {
+        const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + ro);
+        w[0] = r.x;
+        w[1] = r.y;
+      }
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        v[2 * i] += bf16_lo(w[i]);
+        v[2 * i + 1] += bf16_hi(w[i]);
+      }
     }
-    *reinterpret_cast<u32x2*>(a.Y + yo) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    if constexpr (C == 8) *reinterpret_cast<u32x4*>(a.Y + yo) = u32x4{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<u32x2*>(a.Y + yo) = u32x2{w[0], w[1]};
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C; ++i)
     if (n + i < a.N)
       a.Y[yo + i] = (uint16_t)f32_to_bf16_bits(a.R ? v[i] + bf16_to_f32(a.R[ro + i]) : v[i]);
 }

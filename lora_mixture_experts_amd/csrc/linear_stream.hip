@@ -131,10 +131,11 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
         v[w][c] = v[w][c] * linear_scale(a, row) + linear_bias(a, row);
       }
     }
-    f32x4 out;
+    float out[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NW - 1][c]) : linear_act(a.act, v[0][c]);
-    linear_store4(a, t, n, out);
+    for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NW - 1][c]) : v[0][c];
+    if (!GATED) linear_act(a.act, out);
+    linear_store(a, t, n, out);
   }
 }
 

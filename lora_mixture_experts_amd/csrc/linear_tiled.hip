@@ -42,10 +42,10 @@ struct LinearLoader {
   }
 };
 
-template <int BM, int BN, int WM, int WN, bool GATED, bool W8>
+template <int BM, int BN, int WM, int WN, int NST, bool GATED, bool W8>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_kernel(LinearArgs a) {
   constexpr int NWV = (BM / WM) * (BN / WN);
-  using Pipe = TilePipe<BM, BN, WM, WN, 64, 2, false, NWV, W8>;
+  using Pipe = TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>;
   constexpr int FM = Pipe::FM, FN = Pipe::FN, NA = Pipe::NA, NB = Pipe::NB;
   constexpr int ON = GATED ? BN / 2 : BN;  // output columns of a tile
   constexpr int WB = W8 ? 1 : 2;
@@ -131,25 +131,52 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_ke
       }
     return;
   }
-  constexpr int FO = GATED ? FN / 2 : FN;
+
+  // Epilogue through LDS (the stages are free once every wavefront is past the main loop), 32 rows
+  // at a time: each wavefront writes scale * sum + bias row-major into its own region, columns
+  // 32 apart swapped on every other run of 4 rows (the two halves of the wavefront hold rows 4 apart:
+  // different banks), and reads 8 consecutive columns per lane back for the activation, the residual
+  // and a 16-byte store.
+  constexpr int FO = GATED ? FN / 2 : FN, CP = FO * 4;  // output fragments; 8-column pieces of a row
+  float* own = reinterpret_cast<float*>(lds) + wave * (32 * WN);
+  float sc[FN], bi[FN];
 #pragma unroll
-  for (int j = 0; j < FO; ++j) {
-    const int n = col0 + col_of(wn * WN + j * 32 + fr);
-    if (n >= a.N) continue;
-    const float s0v = linear_scale(a, n), b0 = linear_bias(a, n);
-    const float s1v = GATED ? linear_scale(a, (int64_t)n + a.N) : 1.f;
-    const float b1 = GATED ? linear_bias(a, (int64_t)n + a.N) : 0.f;
+  for (int j = 0; j < FN; ++j) {
+    const int r = wn * WN + j * 32 + fr;
+    const int64_t row = col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0);
+    const bool in = col0 + col_of(r) < a.N;
+    sc[j] = in ? linear_scale(a, row) : 1.f;
+    bi[j] = in ? linear_bias(a, row) : 0.f;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+  for (int i = 0; i < FM; ++i) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int tr = row0 + wm * WM + i * 32 + 8 * (v / 4) + 4 * fg + v % 4;
-        if (tr >= a.T) continue;
-        const float g = acc[i][j][v] * s0v + b0;
-        float o = GATED ? swiglu(g, acc[i][(j + FN / 2) % FN][v] * s1v + b1) : linear_act(a.act, g);
-        if (a.R) o += bf16_to_f32(a.R[(int64_t)tr * a.ldr + n]);
-        a.Y[(int64_t)tr * a.ldy + n] = (uint16_t)f32_to_bf16_bits(o);
+    for (int v = 0; v < 16; ++v) {
+      const int r = 8 * (v / 4) + 4 * fg + v % 4;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) own[r * WN + ((j * 32 + fr) ^ (32 * fg))] = acc[i][j][v] * sc[j] + bi[j];
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int it = 0; it < 32 * CP / 64; ++it) {
+      const int idx = it * 64 + lane, r = idx / CP, c = (idx % CP) * 8;
+      const int t = row0 + wm * WM + i * 32 + r, n = col0 + wn * (GATED ? WN / 2 : WN) + c;
+      const float* p = own + r * WN;
+      const int x = 32 * ((r >> 2) & 1);
+      float o[8];
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        const f32x4 g = *reinterpret_cast<const f32x4*>(p + ((c + q) ^ x));
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
+        if (GATED) u = *reinterpret_cast<const f32x4*>(p + ((c + q + WN / 2) ^ x));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[q + e] = GATED ? swiglu(g[e], u[e]) : g[e];
       }
+      if (!GATED) linear_act(a.act, o);
+      if (t < a.T && n < a.N) linear_store(a, t, n, o);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -182,19 +209,22 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearArgs a) {
       v[w][c] = v[w][c] * linear_scale(a, row) + linear_bias(a, row);
     }
   }
-  f32x4 out;
+  float out[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NW - 1][c]) : linear_act(a.act, v[0][c]);
-  linear_store4(a, t, n, out);
+  for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NW - 1][c]) : v[0][c];
+  if (!GATED) linear_act(a.act, out);
+  linear_store(a, t, n, out);
 }
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, bool GATED, bool W8>
+template <int BM, int BN, int WM, int WN, int NST, bool GATED, bool W8>
 hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
   constexpr int NWV = (BM / WM) * (BN / WN);
-  constexpr int bytes = TilePipe<BM, BN, WM, WN, 64, 2, false, NWV, W8>::LDS_BYTES;
-  auto kern = linear_tiled_kernel<BM, BN, WM, WN, GATED, W8>;
+  constexpr int ring = TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>::LDS_BYTES;
+  constexpr int bytes = ring > NWV * 32 * WN * 4 ? ring : NWV * 32 * WN * 4;
+  static_assert(bytes <= kLdsBytes, "LDS stages must fit");
+  auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, GATED, W8>;
   static bool attr_set[64] = {};
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -224,17 +254,31 @@ hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t st
   const int on = gated ? p.bn / 2 : p.bn;
   a.col_tiles = (a.N + on - 1) / on;
   if (a.splits < 1 || (a.splits > 1 && !a.part)) return hipErrorInvalidValue;
-#define MOELORA_LINEAR(BM_, BN_, WM_, WN_)                                                       \
-  if (p.bm == BM_ && p.bn == BN_) {                                                              \
+#define MOELORA_LINEAR(BM_, BN_, WM_, WN_, NST_)                                                \
+  if (p.bm == BM_ && p.bn == BN_ && p.nst == NST_) {                                             \
     if (w8)                                                                                      \
-      return gated ? launch_tile<BM_, BN_, WM_, WN_, true, true>(a, stream)                      \
-                   : launch_tile<BM_, BN_, WM_, WN_, false, true>(a, stream);                    \
-    return gated ? launch_tile<BM_, BN_, WM_, WN_, true, false>(a, stream)                       \
-                 : launch_tile<BM_, BN_, WM_, WN_, false, false>(a, stream);                     \
+      return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, true, true>(a, stream)                \
+                   : launch_tile<BM_, BN_, WM_, WN_, NST_, false, true>(a, stream);              \
+    return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, true, false>(a, stream)                 \
+                 : launch_tile<BM_, BN_, WM_, WN_, NST_, false, false>(a, stream);               \
   }
-  MOELORA_LINEAR(64, 128, 32, 64)
-  MOELORA_LINEAR(128, 128, 32, 64)
-  MOELORA_LINEAR(256, 256, 64, 128)
+  MOELORA_LINEAR(64, 128, 32, 64, 2)
+  MOELORA_LINEAR(128, 128, 32, 64, 2)
+  MOELORA_LINEAR(256, 256, 64, 128, 2)
+#ifdef TUNE
+  MOELORA_LINEAR(32, 64, 32, 64, 4)
+  MOELORA_LINEAR(32, 128, 32, 64, 4)
+  MOELORA_LINEAR(32, 256, 32, 64, 4)
+  MOELORA_LINEAR(64, 64, 32, 64, 4)
+  MOELORA_LINEAR(64, 128, 32, 64, 3)
+  MOELORA_LINEAR(64, 128, 32, 64, 4)
+  MOELORA_LINEAR(64, 256, 32, 64, 2)
+  MOELORA_LINEAR(64, 256, 32, 64, 3)
+  MOELORA_LINEAR(128, 128, 32, 64, 3)
+  MOELORA_LINEAR(128, 128, 32, 64, 4)
+  MOELORA_LINEAR(128, 256, 64, 64, 2)
+  MOELORA_LINEAR(128, 256, 64, 64, 3)
+#endif
 #undef MOELORA_LINEAR
   return hipErrorInvalidValue;
 }
