@@ -277,7 +277,7 @@ int moe_lora_workspace_layout(const moe_lora_dims *d, int32_t topk, moe_lora_lay
 #define MOELORA_GROUP_MAX 0
 #define MOELORA_GROUP_TOP2 1
 typedef struct {
-  int32_t T, n_experts, topk; /* T >= 0; n_experts in [1, 1024]; topk in [1, min(n_experts, 16)] */
+  int32_t T, n_experts, topk; /* T in [0, 2^26); n_experts in [1, 1024]; topk in [1, min(n_experts, 16)] */
   int32_t scoring;            /* MOELORA_SCORE_* */
   int32_t n_groups;           /* divides n_experts, at most 64 */
   int32_t topk_groups;        /* in [1, n_groups]; topk <= topk_groups * n_experts / n_groups */
@@ -315,8 +315,8 @@ int moe_lora_route(const float *logits, const float *bias, const uint8_t *token_
 #define MOELORA_W_BF16 0
 #define MOELORA_W_E4M3 1
 typedef struct {
-  int32_t T, in_features, out_features; /* T >= 0; in_features a positive multiple of 8 (E4M3: of
-                                           16); out_features >= 1 */
+  int32_t T, in_features, out_features; /* T in [0, 2^30); in_features a positive multiple of 8
+                                           (E4M3: of 16); out_features in [1, 2^30) */
   int32_t act;    /* MOELORA_ACT_* */
   int32_t w_type; /* MOELORA_W_BF16, or MOELORA_W_E4M3: OCP E4M3 codes with one scale per row, as
                      in moe_lora_forward_fp8 */

@@ -343,30 +343,53 @@ def sgmv(x, A, B, adapter_ids, y, workspace=None) -> torch.Tensor:
     return y
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
-    """Checks a matrix whose rows may lie apart (their elements adjacent); its row stride."""
+def _refuse(t, name: str, dtype, shape, device: int):
+    """Raises for a tensor that a fast check did not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    row, col = t.stride()
-    if shape[1] > 1 and col != 1:
-        raise ValueError(f"{name}: the elements of a row must be adjacent")
-    if shape[0] <= 1:  # (the stride of a single row means nothing)
-        return max(row, shape[1])
-    if row < shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
-    return row
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
+    raise ValueError(f"{name}: its rows must be dense and must not overlap")
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _dense(t, name: str, dtype, shape, device: int) -> int:
+    """Pointer of a contiguous tensor on GPU `device`, None for None. (These checks run on every call
+    of an operator that takes a few microseconds: they are kept to a few attribute reads.)"""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device >= 0 and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dtype, shape, device: int):
+    """Pointer and row stride of a matrix on GPU `device` whose rows are dense but may lie apart."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0:
+        row, col = t.stride()
+        if col == 1 or shape[1] <= 1:
+            if shape[0] <= 1:  # (the stride of a single row means nothing)
+                return t.data_ptr(), max(row, shape[1])
+            if row >= shape[1]:
+                return t.data_ptr(), row
+    _refuse(t, name, dtype, shape, device)
+
+
+def _on(device: int, call, what: str, *args):
+    """call(*args, stream) with GPU `device` current, on torch's current stream of it."""
+    if torch.cuda.current_device() == device:
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(device))
+    if rc != OK:
+        raise MoeLoraError(rc, what)
 
 
 def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
@@ -382,35 +405,24 @@ def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: i
     receives 1 where a token's logits were not all finite."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a [T][E] tensor")
-    T, E = logits.shape
-    stride = _rows(logits, "logits", torch.float32, (T, E))
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {sorted(SCORINGS)}")
     if group_score not in GROUP_SCORES:
         raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}")
-    if bias is not None:
-        _expect(bias, "bias", torch.float32, (E,))
-    if token_mask is not None:
-        _expect(token_mask, "token_mask", torch.bool, (T,))
-    dev = logits.device
+    T, E = logits.shape
+    dev = logits.get_device()
+    lp, stride = _rows(logits, "logits", torch.float32, (T, E), dev)
     if topk_ids is None:
-        topk_ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
-    else:
-        _expect(topk_ids, "topk_ids", torch.int32, (T, topk))
+        topk_ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=logits.device)
     if topk_w is None:
-        topk_w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
-    else:
-        _expect(topk_w, "topk_w", torch.float32, (T, topk))
-    if token_flags is not None:
-        _expect(token_flags, "token_flags", torch.int32, (T,))
-    _same_device(dev, bias=bias, token_mask=token_mask, topk_ids=topk_ids, topk_w=topk_w,
-                 token_flags=token_flags)
+        topk_w = logits.new_empty((T, max(topk, 0)))
     r = Router(T, E, topk, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score],
                1 if renormalize else 0, scale, stride)
-    with torch.cuda.device(dev):
-        _check(lib().moe_lora_route(_ptr(logits), _ptr(bias), _ptr(token_mask), ctypes.byref(r),
-                                    _ptr(topk_ids), _ptr(topk_w), _ptr(token_flags), _stream(dev)),
-               "moe_lora_route")
+    _on(dev, lib().moe_lora_route, "moe_lora_route", lp, _dense(bias, "bias", torch.float32, (E,), dev),
+        _dense(token_mask, "token_mask", torch.bool, (T,), dev), ctypes.byref(r),
+        _dense(topk_ids, "topk_ids", torch.int32, (T, max(topk, 0)), dev),
+        _dense(topk_w, "topk_w", torch.float32, (T, max(topk, 0)), dev),
+        _dense(token_flags, "token_flags", torch.int32, (T,), dev))
     return topk_ids, topk_w
 
 
@@ -429,31 +441,29 @@ def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
     T, K = x.shape
     rows = W.shape[0]
-    if act == "swiglu" and rows % 2:
-        raise ValueError("W of swiglu has gate and up rows: an even number")
-    N = rows // 2 if act == "swiglu" else rows
+    N = rows
+    if act == "swiglu":
+        if rows % 2:
+            raise ValueError("W of swiglu has gate and up rows: an even number")
+        N = rows // 2
     bf = torch.bfloat16
-    xs = _rows(x, "x", bf, (T, K))
-    ws = _rows(W, "W", bf if w_scale is None else torch.uint8, (rows, K))
-    if w_scale is not None:
-        _expect(w_scale, "w_scale", torch.float32, (rows,))
-    if bias is not None:
-        _expect(bias, "bias", bf, (rows,))
-    rs = _rows(residual, "residual", bf, (T, N)) if residual is not None else 0
-    dev = x.device
+    dev = x.get_device()
+    xp, xs = _rows(x, "x", bf, (T, K), dev)
+    wp, ws = _rows(W, "W", bf if w_scale is None else torch.uint8, (rows, K), dev)
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", bf, (T, N), dev)
     if y is None:
-        y = torch.empty((T, N), dtype=bf, device=dev)
-    ys = _rows(y, "y", bf, (T, N))
+        y = x.new_empty((T, N))
+    yp, ys = _rows(y, "y", bf, (T, N), dev)
     d = LinearDims(T, K, N, ACTIVATIONS[act], 0 if w_scale is None else 1, xs, ws, ys, rs)
-    L = lib()
-    need = L.moe_lora_linear_workspace_size(ctypes.byref(d))
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _same_device(dev, W=W, w_scale=w_scale, bias=bias, residual=residual, y=y, workspace=workspace)
-    with torch.cuda.device(dev):
-        _check(L.moe_lora_linear(_ptr(x), _ptr(W), _ptr(w_scale), _ptr(bias), _ptr(residual), ctypes.byref(d),
-                                 _ptr(y), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                 _stream(dev)), "moe_lora_linear")
+    L, dp = lib(), ctypes.byref(d)
+    if workspace is None:
+        need = L.moe_lora_linear_workspace_size(dp)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    kp, kb = (None, 0) if workspace is None else (
+        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel())
+    _on(dev, L.moe_lora_linear, "moe_lora_linear", xp, wp, _dense(w_scale, "w_scale", torch.float32, (rows,), dev),
+        _dense(bias, "bias", bf, (rows,), dev), rp, dp, yp, kp, kb)
     return y
 
 

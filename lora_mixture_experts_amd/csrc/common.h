@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace moelora {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -45,20 +47,16 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-// Eight E4M3 codes (half `hi` of the 16 in v, bytes in K order) as one bf16 MFMA operand. The
-// hardware conversion decodes the OCP E4M3 format into float32; the bf16 is its upper half
-// (exact, as E4M3 has 3 mantissa bits and a narrower exponent range).
+// Eight E4M3 codes (half `hi` of the 16 in v, bytes in K order) as one bf16 MFMA operand: the
+// hardware conversion of two OCP E4M3 codes at a scale of 1 (exact, as E4M3 has 3 mantissa bits and
+// a narrower exponent range).
 __device__ __forceinline__ u32x4 e4m3x8_to_bf16(u32x4 v, int hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
   const uint32_t d0 = hi ? v.z : v.x, d1 = hi ? v.w : v.y;
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)d0, false);
-  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)d0, true);
-  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)d1, false);
-  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)d1, true);
-  auto pack = [](f32x2 f) {
-    return __builtin_amdgcn_perm(__float_as_uint(f.y), __float_as_uint(f.x), 0x07060302u);
+  auto pair = [](uint32_t d, auto up) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.f, decltype(up)::value));
   };
-  return u32x4{pack(a), pack(b), pack(c), pack(d)};
+  return u32x4{pair(d0, std::false_type{}), pair(d0, std::true_type{}), pair(d1, std::false_type{}),
+               pair(d1, std::true_type{})};
 }
 
 __device__ __forceinline__ u32x4 ldg16(const void* p) {

@@ -169,6 +169,7 @@ struct SgmvArgs {
 // 2 N rows, gate then up.
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSwiglu = 5 };
 constexpr int kLinearStreamTokens = 64;  // token rows the weight-streaming kernel takes
+constexpr int kMaxLinearSplits = 8;      // of the reduction
 struct LinearArgs {
   const uint16_t* X;    // [T] rows of K bf16, ldx apart
   const void* W;        // [rows] rows of K bf16, or E4M3 codes when wscale is given, ldw apart
@@ -188,6 +189,7 @@ struct LinearArgs {
 struct LinearPlan {
   bool stream;
   int bm, bn, nst;  // tile and LDS stages
+  int kg;           // groups of wavefronts that share a tile's reduction
   int splits;       // of the reduction
 };
 

@@ -35,48 +35,73 @@ __device__ __forceinline__ void linear_act(int act, float (&v)[C]) {
 }
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-// C (4 or 8) consecutive output columns n.. of token row t: residual, rounding and store, as one
-// access of 2 C bytes where the rows of y and of the residual allow it (a.vec: the largest access
-// in bytes that their strides and addresses do).
+// What the epilogue adds to C (4 or 8) consecutive output columns n.. of token row t: loaded ahead
+// of the sums so that its latency hides behind theirs. One access of 2 C bytes where the rows of
+// the residual and of y allow it (a.vec: the largest access in bytes that their strides and
+// addresses do). Nothing is read past the row's end.
 template <int C>
-__device__ __forceinline__ void linear_store(const LinearArgs& a, int t, int n, float (&v)[C]) {
-  const int64_t yo = (int64_t)t * a.ldy + n, ro = (int64_t)t * a.ldr + n;
-  if (a.vec >= 2 * C && n + C <= a.N) {
-    uint32_t w[C / 2];
-    if (a.R) {
+struct Residual {
+  uint32_t w[C / 2];
+  __device__ __forceinline__ void load(const LinearArgs& a, int t, int n) {
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) w[i] = 0u;
+    if (!a.R || t >= a.T) return;
+    const uint16_t* p = a.R + (int64_t)t * a.ldr + n;
+    if (a.vec >= 2 * C && n + C <= a.N) {
       if constexpr (C == 8) {
-        const u32x4 r = *reinterpret_cast<const u32x4*>(a.R + ro);
+        const u32x4 r = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = r[i];
       } else {
-        const u32x2 r = *reinterpret_cast<const u32x2*>(a.R + ro);
+        const u32x2 r = *reinterpret_cast<const u32x2*>(p);
         w[0] = r.x;
         w[1] = r.y;
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        v[2 * i] += bf16_lo(w[i]);
-        v[2 * i + 1] += bf16_hi(w[i]);
-      }
+      for (int i = 0; i < C; ++i)
+        if (n + i < a.N) w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
     }
+  }
+};
+
+// C columns of y: plus the residual, rounded, stored. (No residual: -0 stays -0.)
+template <int C>
+__device__ __forceinline__ void linear_store(const LinearArgs& a, int t, int n, float (&v)[C],
+                                             const Residual<C>& r) {
+  if (t >= a.T || n >= a.N) return;
+  if (a.R) {
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      v[2 * i] += bf16_lo(r.w[i]);
+      v[2 * i + 1] += bf16_hi(r.w[i]);
+    }
+  }
+  uint16_t* y = a.Y + (int64_t)t * a.ldy + n;
+  if (a.vec >= 2 * C && n + C <= a.N) {
+    uint32_t w[C / 2];
 #pragma unroll
     for (int i = 0; i < C / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    if constexpr (C == 8) *reinterpret_cast<u32x4*>(a.Y + yo) = u32x4{w[0], w[1], w[2], w[3]};
-    else *reinterpret_cast<u32x2*>(a.Y + yo) = u32x2{w[0], w[1]};
-    return;
-  }
+    if constexpr (C == 8) *reinterpret_cast<u32x4*>(y) = u32x4{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<u32x2*>(y) = u32x2{w[0], w[1]};
+  } else {
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-    if (n + i < a.N)
-      a.Y[yo + i] = (uint16_t)f32_to_bf16_bits(a.R ? v[i] + bf16_to_f32(a.R[ro + i]) : v[i]);
+    for (int i = 0; i < C; ++i)
+      if (n + i < a.N) y[i] = (uint16_t)f32_to_bf16_bits(v[i]);
+  }
 }
 
-// Scale and bias of weight row w (a row past the end: none).
-__device__ __forceinline__ float linear_scale(const LinearArgs& a, int64_t w) {
-  return a.wscale && w < a.rows ? a.wscale[w] : 1.f;
-}
-__device__ __forceinline__ float linear_bias(const LinearArgs& a, int64_t w) {
-  return a.bias && w < a.rows ? bf16_to_f32(a.bias[w]) : 0.f;
-}
+// Scales and biases of C consecutive weight rows w..w+C-1 (rows past `end`: 1 and 0).
+template <int C>
+struct ScaleBias {
+  float s[C], b[C];
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t w, int64_t end) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      s[c] = a.wscale && w + c < end ? a.wscale[w + c] : 1.f;
+      b[c] = a.bias && w + c < end ? bf16_to_f32(a.bias[w + c]) : 0.f;
+    }
+  }
+};
 
 }  // namespace moelora

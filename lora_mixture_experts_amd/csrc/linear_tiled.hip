@@ -4,12 +4,17 @@
 // y[t][n] = act(scale[n] * sum_k x[t][k] W[n][k] + bias[n]) + r[t][n], BM token rows x BN weight
 // rows per workgroup. The main loop is the layer's (TilePipe: operand tiles straight from HBM into
 // a ring of LDS stages). SwiGLU: the weight rows of a wavefront's column range are
-// [gate i .. | up i ..] for the same outputs i, so a lane holds both. Bound by the MFMAs for
-// prompts, by the weight bytes below some 300 tokens.
+// [gate i .. | up i ..] for the same outputs i, so a lane holds both.
 //
-// Where the tiles would leave most of the chip idle the reduction is split: split s of a tile
-// stores its fp32 sums into the workspace, and a second kernel adds them in split order and applies
-// the epilogue (the result does not depend on timing).
+// What bounds it: the MFMAs in 256 x 256 tiles (a 64-wide step of a lone tile takes 1.05 us for
+// 0.9 us of MFMAs); in smaller tiles what one CU can draw through its L1, 80 to 90 GB/s whatever the
+// ring's depth (64 x 128 tiles: 0.53 us for two steps). So small batches spread over the CUs, first in
+// the workgroup: KG groups of wavefronts, each with a ring of its own, take an equal share of the
+// reduction and their sums meet in the epilogue's LDS (256 x 2048 x 1536, 96 tiles: 15.7 us with
+// one group, 12.5 with four; a second launch would cost 4 us). Where the tiles would still leave
+// most of the chip idle the reduction is split over workgroups too: split s of a tile stores its
+// fp32 sums into the workspace, and a second kernel adds them in split order and applies the
+// epilogue. No order of additions depends on timing.
 #include "common.h"
 #include "kernels.h"
 #include "linear.h"
@@ -36,14 +41,15 @@ struct LinearLoader {
     if (ks < full) {
       load_main(d, ks, lds_addr);
     } else {
-      if (d < NA) lds_dma16(xr, xe[d], (uint32_t)ks * BKS * 2, lds_addr);
-      else lds_dma16(wr[d - NA], we[d - NA], (uint32_t)ks * Pipe::BROW, lds_addr);
+      // (steps past the partial one: a K group with fewer steps than the others, all zeros)
+      if (d < NA) lds_dma16(xr, ks == full ? xe[d] : kOutOfRange, (uint32_t)ks * BKS * 2, lds_addr);
+      else lds_dma16(wr[d - NA], ks == full ? we[d - NA] : kOutOfRange, (uint32_t)ks * Pipe::BROW, lds_addr);
     }
   }
 };
 
-template <int BM, int BN, int WM, int WN, int NST, bool GATED, bool W8>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_kernel(LinearArgs a) {
+template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8>
+__global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_tiled_kernel(LinearArgs a) {
   constexpr int NWV = (BM / WM) * (BN / WN);
   using Pipe = TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>;
   constexpr int FM = Pipe::FM, FN = Pipe::FN, NA = Pipe::NA, NB = Pipe::NB;
@@ -53,7 +59,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_ke
   static_assert(!GATED || (WN / 2) % Pipe::RPBB == 0, "a load block is all gate or all up rows");
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wave_all / NWV, wave = wave_all % NWV;  // K group, wavefront of the tile
   const int wm = wave / Pipe::WAVES_N, wn = wave % Pipe::WAVES_N;
 
   // Workgroup ids go round-robin over the 8 XCDs: each takes a contiguous range of the tiles,
@@ -71,11 +78,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_ke
   const int rt = rg * 4 + w % rows, ct = cg * 4 + w / rows;
   const int row0 = rt * BM, col0 = ct * ON;
 
-  // this split's K range in whole 64-wide steps
+  // this split's K range in whole 64-wide steps, an equal share of it for each K group (the last
+  // ones may have less, or nothing, to load)
   const int nsteps_all = (a.K + 63) / 64;
   const int s0 = (int)((int64_t)nsteps_all * sp / a.splits);
   const int s1 = (int)((int64_t)nsteps_all * (sp + 1) / a.splits);
-  const int k0 = s0 * 64, klen = min(a.K, s1 * 64) - k0;
+  int nsteps = (s1 - s0 + KG - 1) / KG;
+  const int k0 = min(s0 + kg * nsteps, s1) * 64;
+  const int klen = max(0, min(a.K, min(s0 + (kg + 1) * nsteps, s1) * 64) - k0);
 
   // weight row of tile row r: output column col0 + c of the gate or up half
   auto col_of = [&](int r) { return GATED ? (r / WN) * (WN / 2) + r % (WN / 2) : r; };
@@ -108,123 +118,191 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void linear_tiled_ke
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  int nsteps = s1 - s0;
-  Pipe::run_steps(acc, ld, lds, nsteps, wave, lane, [] {});
-
-  // lane: rows 8*(v/4) + 4*(lane/32) + v%4 of each 32-row group, column lane%32 of each fragment
-  const int fr = lane & 31, fg = lane >> 5;
-  if (a.splits > 1) {
-    float* part = a.part + (int64_t)sp * a.T * a.rows;
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int r = wn * WN + j * 32 + fr;
-        const int n = col0 + col_of(r);
-        if (n >= a.N) continue;
-        const int64_t wrow = n + (is_up(r) ? (int64_t)a.N : 0);
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int tr = row0 + wm * WM + i * 32 + 8 * (v / 4) + 4 * fg + v % 4;
-          if (tr < a.T) part[(int64_t)tr * a.rows + wrow] = acc[i][j][v];
-        }
-      }
-    return;
-  }
+  Pipe::run_steps(acc, ld, lds + kg * (Pipe::LDS_BYTES / 2), nsteps, wave, lane, [] {});
 
   // Epilogue through LDS (the stages are free once every wavefront is past the main loop), 32 rows
-  // at a time: each wavefront writes scale * sum + bias row-major into its own region, columns
-  // 32 apart swapped on every other run of 4 rows (the two halves of the wavefront hold rows 4 apart:
-  // different banks), and reads 8 consecutive columns per lane back for the activation, the residual
-  // and a 16-byte store.
-  constexpr int FO = GATED ? FN / 2 : FN, CP = FO * 4;  // output fragments; 8-column pieces of a row
-  float* own = reinterpret_cast<float*>(lds) + wave * (32 * WN);
+  // at a time. A lane holds rows 8*(v/4) + 4*(lane/32) + v%4 of each 32-row group and column lane%32
+  // of each fragment: each wavefront writes scale * sum (+ bias) row-major into its own region,
+  // columns 32 apart swapped on every other run of 4 rows (the two halves of the wavefront hold rows 4
+  // apart: different banks). Then a lane reads 8 columns back, of all K groups, and finishes them:
+  // 8 consecutive ones where 16-byte accesses of y and the residual are possible, else columns 64
+  // apart, so that a store covers 128 consecutive bytes. The residual's loads go out before the values
+  // are written.
+  const int fr = lane & 31, fg = lane >> 5;
+  constexpr int FO = GATED ? FN / 2 : FN, OC = FO * 32;  // output fragments and columns
+  constexpr int TP = 32 * OC / 512, ITS = (TP + KG - 1) / KG;  // pieces of 8 columns per lane: all, a group's
+  constexpr int REGION = 32 * WN;                        // floats
+  float* const all = reinterpret_cast<float*>(lds);
+  float* const own = all + wave_all * REGION;
+  const bool split = a.splits > 1, wide = a.vec >= 16;
   float sc[FN], bi[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int r = wn * WN + j * 32 + fr;
     const int64_t row = col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0);
-    const bool in = col0 + col_of(r) < a.N;
-    sc[j] = in ? linear_scale(a, row) : 1.f;
-    bi[j] = in ? linear_bias(a, row) : 0.f;
+    ScaleBias<1> sb;
+    sb.load(a, row, !split && col0 + col_of(r) < a.N ? row + 1 : row);
+    sc[j] = sb.s[0];
+    bi[j] = kg == 0 ? sb.b[0] : 0.f;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
+    const int tr = row0 + wm * WM + i * 32, tc = col0 + wn * OC;
+    Residual<8> res[ITS];
+    if (!split && wide) {
+#pragma unroll
+      for (int it = 0; it < ITS; ++it) {
+        if (it * KG + kg >= TP) continue;
+        const int f = ((it * KG + kg) * 64 + lane) * 8;
+        res[it].load(a, tr + f / OC, tc + f % OC);
+      }
+    }
+    if (KG > 1 && i > 0) __syncthreads();  // the other groups have read the rows before
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int r = 8 * (v / 4) + 4 * fg + v % 4;
 #pragma unroll
       for (int j = 0; j < FN; ++j) own[r * WN + ((j * 32 + fr) ^ (32 * fg))] = acc[i][j][v] * sc[j] + bi[j];
     }
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int it = 0; it < 32 * CP / 64; ++it) {
-      const int idx = it * 64 + lane, r = idx / CP, c = (idx % CP) * 8;
-      const int t = row0 + wm * WM + i * 32 + r, n = col0 + wn * (GATED ? WN / 2 : WN) + c;
-      const float* p = own + r * WN;
-      const int x = 32 * ((r >> 2) & 1);
-      float o[8];
+    if (KG > 1) __syncthreads();
+    else __builtin_amdgcn_wave_barrier();
+    // column c of row r, all K groups (WN/2 further: the up half)
+    auto sum4 = [&](int r, int c) {
+      const float* p = all + wave * REGION + r * WN + (c ^ (32 * ((r >> 2) & 1)));
+      f32x4 s = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
-      for (int q = 0; q < 8; q += 4) {
-        const f32x4 g = *reinterpret_cast<const f32x4*>(p + ((c + q) ^ x));
-        f32x4 u = {0.f, 0.f, 0.f, 0.f};
-        if (GATED) u = *reinterpret_cast<const f32x4*>(p + ((c + q + WN / 2) ^ x));
+      for (int g = 1; g < KG; ++g) s += *reinterpret_cast<const f32x4*>(p + g * NWV * REGION);
+      return s;
+    };
+    auto sum1 = [&](int r, int c) {
+      const float* p = all + wave * REGION + r * WN + (c ^ (32 * ((r >> 2) & 1)));
+      float s = *p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[q + e] = GATED ? swiglu(g[e], u[e]) : g[e];
+      for (int g = 1; g < KG; ++g) s += p[g * NWV * REGION];
+      return s;
+    };
+    if (split) {
+      float* part = a.part + (int64_t)sp * a.T * a.rows;
+#pragma unroll 4
+      for (int f0 = kg * 64; f0 < 32 * WN; f0 += KG * 64) {
+        const int r = (f0 + lane) / WN, c = (f0 + lane) % WN;
+        const int n = tc + (GATED ? c % (WN / 2) : c);
+        if (tr + r < a.T && n < a.N)
+          part[(int64_t)(tr + r) * a.rows + n + (GATED && c >= WN / 2 ? (int64_t)a.N : 0)] = sum1(r, c);
       }
-      if (!GATED) linear_act(a.act, o);
-      if (t < a.T && n < a.N) linear_store(a, t, n, o);
+    } else if (wide) {
+      if (!GATED && KG == 1 && a.act != kActNone) {
+        // (a loop that is not unrolled: unrolled over the accumulators, activations spilled them)
+#pragma unroll 1
+        for (int it = 0; it < ITS; ++it) {
+          float* p = own + (it * 64 + lane) * 8;  // (any share of the values will do)
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = p[e];
+          linear_act(a.act, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = o[e];
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int it = 0; it < ITS; ++it) {
+        if (it * KG + kg >= TP) continue;
+        const int f = ((it * KG + kg) * 64 + lane) * 8, r = f / OC, c = f % OC;
+        float o[8];
+#pragma unroll
+        for (int q = 0; q < 8; q += 4) {
+          const f32x4 g = sum4(r, c + q);
+          f32x4 u = {0.f, 0.f, 0.f, 0.f};
+          if (GATED) u = sum4(r, c + q + WN / 2);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[q + e] = GATED ? swiglu(g[e], u[e]) : g[e];
+        }
+        if (!GATED && KG > 1) linear_act(a.act, o);
+        linear_store(a, tr + r, tc + c, o, res[it]);
+      }
+    } else {
+#pragma unroll 1
+      for (int it = 0; it < ITS; ++it) {
+        if (it * KG + kg >= TP) break;
+        const int f = (it * KG + kg) * 512 + lane;
+        float o[8], add[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = (f + 64 * e) / OC, c = (f + 64 * e) % OC, t = tr + r, n = tc + c;
+          add[e] = a.R && t < a.T && n < a.N ? bf16_to_f32(a.R[(int64_t)t * a.ldr + n]) : 0.f;
+          const float g = sum1(r, c);
+          o[e] = GATED ? swiglu(g, sum1(r, c + WN / 2)) : g;
+        }
+        if (!GATED) linear_act(a.act, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = (f + 64 * e) / OC, c = (f + 64 * e) % OC, t = tr + r, n = tc + c;
+          if (t < a.T && n < a.N)
+            a.Y[(int64_t)t * a.ldy + n] = (uint16_t)f32_to_bf16_bits(a.R ? o[e] + add[e] : o[e]);
+        }
+      }
     }
-    __builtin_amdgcn_wave_barrier();
+    if (KG == 1) __builtin_amdgcn_wave_barrier();
   }
 }
 
-// Sums of the splits, then the epilogue: one thread per 4 output columns of a token.
+// Sums of the splits, then the epilogue: one thread per 4 output columns of a token. The loads of up
+// to kMaxLinearSplits splits go out before the first addition (those past the last split read the
+// last again and are not added).
 template <bool GATED>
 __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearArgs a) {
-  constexpr int NW = GATED ? 2 : 1;
+  constexpr int NH = GATED ? 2 : 1;
   const int nq = (a.N + 3) / 4;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= (int64_t)a.T * nq) return;
   const int t = (int)(idx / nq), n = (int)(idx - (int64_t)t * nq) * 4;
-  f32x4 v[NW];
+  ScaleBias<4> sb[NH];
+  Residual<4> res;
+  const int64_t stride = (int64_t)a.T * a.rows;
+  f32x4 p[NH][kMaxLinearSplits];
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const float* p = a.part + (int64_t)t * a.rows + (int64_t)w * a.N + n;
-    const int64_t stride = (int64_t)a.T * a.rows;
-    v[w] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int have = min(4, a.N - n);
+  for (int h = 0; h < NH; ++h) {
+    const float* src = a.part + (int64_t)t * a.rows + (int64_t)h * a.N + n;
     if (a.rows % 4 == 0 && a.N % 4 == 0) {
-      for (int s = 0; s < a.splits; ++s) v[w] += *reinterpret_cast<const f32x4*>(p + s * stride);
+#pragma unroll
+      for (int s = 0; s < kMaxLinearSplits; ++s)
+        p[h][s] = *reinterpret_cast<const f32x4*>(src + min(s, a.splits - 1) * stride);
     } else {
-      for (int s = 0; s < a.splits; ++s)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < have) v[w][c] += p[s * stride + c];
-    }
+      for (int s = 0; s < kMaxLinearSplits; ++s)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t row = (int64_t)w * a.N + n + c;
-      v[w][c] = v[w][c] * linear_scale(a, row) + linear_bias(a, row);
+        for (int c = 0; c < 4; ++c) p[h][s][c] = src[min(s, a.splits - 1) * stride + min(c, a.N - 1 - n)];
     }
+    sb[h].load(a, (int64_t)h * a.N + n, (int64_t)(h + 1) * a.N);
   }
-  float out[4];
+  res.load(a, t, n);
+  float out[4], v[NH][4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NW - 1][c]) : v[0][c];
+  for (int h = 0; h < NH; ++h) {
+#pragma unroll
+    for (int s = 1; s < kMaxLinearSplits; ++s)
+      if (s < a.splits) p[h][0] += p[h][s];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[h][c] = p[h][0][c] * sb[h].s[c] + sb[h].b[c];
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) out[c] = GATED ? swiglu(v[0][c], v[NH - 1][c]) : v[0][c];
   if (!GATED) linear_act(a.act, out);
-  linear_store(a, t, n, out);
+  linear_store(a, t, n, out, res);
 }
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, int NST, bool GATED, bool W8>
+template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8>
 hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
   constexpr int NWV = (BM / WM) * (BN / WN);
-  constexpr int ring = TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>::LDS_BYTES;
-  constexpr int bytes = ring > NWV * 32 * WN * 4 ? ring : NWV * 32 * WN * 4;
+  constexpr int ring = KG * TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>::LDS_BYTES;
+  constexpr int out = KG * NWV * 32 * WN * 4;  // the epilogue's regions
+  constexpr int bytes = ring > out ? ring : out;
   static_assert(bytes <= kLdsBytes, "LDS stages must fit");
-  auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, GATED, W8>;
+  auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, KG, GATED, W8>;
   static bool attr_set[64] = {};
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -235,8 +313,9 @@ hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
     attr_set[dev] = true;
   }
   const int64_t live = (int64_t)a.row_tiles * a.col_tiles * a.splits;
+  if (live * 64 * NWV * KG >= ((int64_t)1 << 32) - 4096) return hipErrorInvalidValue;  // threads of a launch
   const unsigned grid = (unsigned)((live + 7) / 8 * 8);
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * NWV), bytes, stream, a);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * NWV * KG), bytes, stream, a);
   err = hipGetLastError();
   if (err != hipSuccess || a.splits == 1) return err;
   const int64_t n = (int64_t)a.T * ((a.N + 3) / 4);
@@ -253,32 +332,19 @@ hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t st
   a.row_tiles = (a.T + p.bm - 1) / p.bm;
   const int on = gated ? p.bn / 2 : p.bn;
   a.col_tiles = (a.N + on - 1) / on;
-  if (a.splits < 1 || (a.splits > 1 && !a.part)) return hipErrorInvalidValue;
-#define MOELORA_LINEAR(BM_, BN_, WM_, WN_, NST_)                                                \
-  if (p.bm == BM_ && p.bn == BN_ && p.nst == NST_) {                                             \
+  if (a.splits < 1 || a.splits > kMaxLinearSplits || (a.splits > 1 && !a.part)) return hipErrorInvalidValue;
+#define MOELORA_LINEAR(BM_, BN_, WM_, WN_, NST_, KG_)                                           \
+  if (p.bm == BM_ && p.bn == BN_ && p.nst == NST_ && p.kg == KG_) {                              \
     if (w8)                                                                                      \
-      return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, true, true>(a, stream)                \
-                   : launch_tile<BM_, BN_, WM_, WN_, NST_, false, true>(a, stream);              \
-    return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, true, false>(a, stream)                 \
-                 : launch_tile<BM_, BN_, WM_, WN_, NST_, false, false>(a, stream);               \
+      return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, KG_, true, true>(a, stream)           \
+                   : launch_tile<BM_, BN_, WM_, WN_, NST_, KG_, false, true>(a, stream);         \
+    return gated ? launch_tile<BM_, BN_, WM_, WN_, NST_, KG_, true, false>(a, stream)            \
+                 : launch_tile<BM_, BN_, WM_, WN_, NST_, KG_, false, false>(a, stream);          \
   }
-  MOELORA_LINEAR(64, 128, 32, 64, 2)
-  MOELORA_LINEAR(128, 128, 32, 64, 2)
-  MOELORA_LINEAR(256, 256, 64, 128, 2)
-#ifdef TUNE
-  MOELORA_LINEAR(32, 64, 32, 64, 4)
-  MOELORA_LINEAR(32, 128, 32, 64, 4)
-  MOELORA_LINEAR(32, 256, 32, 64, 4)
-  MOELORA_LINEAR(64, 64, 32, 64, 4)
-  MOELORA_LINEAR(64, 128, 32, 64, 3)
-  MOELORA_LINEAR(64, 128, 32, 64, 4)
-  MOELORA_LINEAR(64, 256, 32, 64, 2)
-  MOELORA_LINEAR(64, 256, 32, 64, 3)
-  MOELORA_LINEAR(128, 128, 32, 64, 3)
-  MOELORA_LINEAR(128, 128, 32, 64, 4)
-  MOELORA_LINEAR(128, 256, 64, 64, 2)
-  MOELORA_LINEAR(128, 256, 64, 64, 3)
-#endif
+  MOELORA_LINEAR(64, 64, 32, 64, 2, 4)
+  MOELORA_LINEAR(64, 128, 32, 64, 3, 2)
+  MOELORA_LINEAR(128, 128, 32, 64, 3, 1)
+  MOELORA_LINEAR(256, 256, 64, 128, 2, 1)
 #undef MOELORA_LINEAR
   return hipErrorInvalidValue;
 }

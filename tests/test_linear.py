@@ -262,7 +262,7 @@ def _call(ws_bytes=1 << 40, ptrs=None, **kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(in_features=0), dict(in_features=508), dict(out_features=0), dict(act=6), dict(act=-1),
+    dict(T=-1), dict(T=1 << 30), dict(in_features=0), dict(in_features=508), dict(out_features=0), dict(act=6), dict(act=-1),
     dict(w_type=2), dict(x_stride=504), dict(x_stride=516), dict(w_stride=500), dict(w_stride=516),
     dict(y_stride=63), dict(residual_stride=63), dict(x_stride=1 << 22), dict(w_stride=1 << 22),
     dict(y_stride=1 << 22), dict(w_type=1, in_features=504, w_stride=512), dict(w_type=1, w_stride=520)])

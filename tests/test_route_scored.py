@@ -219,7 +219,7 @@ def _call(ptrs=None, **kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(n_experts=0), dict(n_experts=1025, logits_stride=1025), dict(topk=0), dict(topk=17),
+    dict(T=-1), dict(T=1 << 26), dict(n_experts=0), dict(n_experts=1025, logits_stride=1025), dict(topk=0), dict(topk=17),
     dict(n_experts=4, topk=5), dict(scoring=2), dict(scoring=-1), dict(n_groups=0), dict(n_groups=3),
     dict(n_experts=130, n_groups=65, topk_groups=65, logits_stride=130), dict(topk_groups=0),
     dict(n_groups=4, topk_groups=5), dict(n_groups=16, topk_groups=1), dict(group_score=2), dict(renormalize=2),
