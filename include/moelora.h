@@ -61,6 +61,7 @@ extern "C" {
 /* Device-side flags reported by moe_lora_debug_status. */
 #define MOELORA_FLAG_NONFINITE_LOGIT 1u
 #define MOELORA_FLAG_ADAPTER_RANGE 2u
+#define MOELORA_FLAG_EXPERT_RANGE 4u /* moe_lora_forward_topk: an expert id outside [-1, E) */
 
 /* Layer sizes (page "vLLM MoE LoRA SageMaker Bedrock", sections "Entendendo os Modelos MoE" and
  * "O Papel da Multi-LoRA": T tokens of width hidden, n_experts experts of intermediate width
@@ -228,7 +229,7 @@ int moe_lora_route_align(const float *router_logits, const int32_t *adapter_ids,
                          int64_t sorted_cap, int32_t *expert_offsets, int32_t *seg_table,
                          int32_t *n_seg, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Where moe_lora_forward (and its _timed, _routed and _fp8 variants) keeps the sorted layout of a
+/* Where moe_lora_forward (and its _timed, _routed, _fp8 and _topk variants) keeps the sorted layout of a
  * call inside the workspace, so that a caller can read the layer's own routing tables back after
  * a call and check them (page "vLLM MoE LoRA SageMaker Bedrock", section "Implementação Técnica
  * no vLLM": token-expert pairs grouped by expert and, inside an expert, by adapter). Offsets are
@@ -240,7 +241,8 @@ int moe_lora_route_align(const float *router_logits, const int32_t *adapter_ids,
  *   n_blocks [1]              padded total / block_m
  *   block_expert [n_blocks]   expert of each row block
  *   block_seg [n_blocks]      segment holding the block's first row, -1 when that row is padding
- *   pair_row [T*topk]         sorted row of each pair
+ *   pair_row [T*topk]         sorted row of each pair (moe_lora_forward_topk: -1 for an empty slot;
+ *                             it leaves topk_ids and topk_w unwritten)
  *   sorted_ad [capacity]      adapter of each sorted row, -1 for none and for padding rows
  * Only the rows below the padded total are defined. Host-only: touches no device memory.
  * Returns MOELORA_OK, or the error moe_lora_workspace_size would meet (MOELORA_ENULL for a NULL
@@ -297,6 +299,22 @@ typedef struct {
 int moe_lora_route(const float *logits, const float *bias, const uint8_t *token_mask,
                    const moe_lora_router *r, int32_t *topk_ids, float *topk_w,
                    int32_t *token_flags, void *stream);
+
+/* moe_lora_forward with the experts and weights of every token given, as by moe_lora_route (page
+ * "vLLM MoE LoRA SageMaker Bedrock", section "Entendendo os Modelos MoE": the outputs of the
+ * experts a token was sent to are aggregated): y[t] = sum_j topk_w[t][j] * expert topk_ids[t][j] of
+ * x[t], in slot order. topk_ids int32 [T][topk], in [-1, n_experts): -1 is an empty slot, which adds
+ * nothing (its weight is not used; a token with empty slots only gets y = 0); an id outside that
+ * range is taken as -1 and sets MOELORA_FLAG_EXPERT_RANGE. A token may name an expert twice. topk_w
+ * f32 [T][topk]. W1_scale and W2_scale NULL: bf16 W1 and W2; both given: E4M3 codes and scales, as
+ * in moe_lora_forward_fp8. Everything else (layouts, workspace and its size, flags, errors) as in
+ * moe_lora_forward. */
+int moe_lora_forward_topk(const void *x, const int32_t *topk_ids, const float *topk_w,
+                          const void *W1, const float *W1_scale, const void *W2,
+                          const float *W2_scale, const void *A1, const void *B1, const void *A2,
+                          const void *B2, const int32_t *adapter_ids, int32_t topk,
+                          const moe_lora_dims *d, void *y, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /* Dense projection with its epilogue (page "vLLM MoE LoRA SageMaker Bedrock", section "O Papel da
  * Multi-LoRA": the frozen product xW that moe_lora_sgmv adds a batch's adapters to; section

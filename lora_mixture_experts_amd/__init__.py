@@ -17,13 +17,13 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoelora.so")
 
 OK, EINVAL_DIMS, ENULL, EALIGN, EWORKSPACE, EHIP, EDEVICE, EUNSUPPORTED, ESCRATCH = 0, -1, -2, -3, -4, -5, -6, -7, -8
-FLAG_NONFINITE_LOGIT, FLAG_ADAPTER_RANGE = 1, 2
+FLAG_NONFINITE_LOGIT, FLAG_ADAPTER_RANGE, FLAG_EXPERT_RANGE = 1, 2, 4
 
 EXPORTS = ("moe_lora_workspace_size", "moe_lora_forward", "moe_lora_forward_timed", "moe_lora_forward_fp8",
            "moe_lora_sorted_capacity", "moe_lora_route_align", "moe_lora_strerror",
            "moe_lora_debug_status", "moe_lora_sgmv_workspace_size", "moe_lora_sgmv",
            "moe_lora_router_logits", "moe_lora_forward_routed", "moe_lora_workspace_layout",
-           "moe_lora_route", "moe_lora_linear", "moe_lora_linear_workspace_size",
+           "moe_lora_route", "moe_lora_forward_topk", "moe_lora_linear", "moe_lora_linear_workspace_size",
            "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
 N_STAGES = 7
 STAGES = ("route", "align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
@@ -110,6 +110,8 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_workspace_layout.restype = ctypes.c_int
         L.moe_lora_route.argtypes = [P, P, P, ctypes.POINTER(Router), P, P, P, P]
         L.moe_lora_route.restype = ctypes.c_int
+        L.moe_lora_forward_topk.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, i32, D, P, P, ctypes.c_size_t, P]
+        L.moe_lora_forward_topk.restype = ctypes.c_int
         L.moe_lora_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDims)]
         L.moe_lora_linear_workspace_size.restype = ctypes.c_size_t
         L.moe_lora_linear.argtypes = [P, P, P, P, P, ctypes.POINTER(LinearDims), P, P, ctypes.c_size_t, P]
@@ -424,6 +426,36 @@ def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: i
         _dense(topk_w, "topk_w", torch.float32, (T, max(topk, 0)), dev),
         _dense(token_flags, "token_flags", torch.int32, (T,), dev))
     return topk_ids, topk_w
+
+
+def forward_topk(x, topk_ids, topk_w, W1, W2, A1, B1, A2, B2, adapter_ids, *, W1_scale=None, W2_scale=None,
+                 y=None, workspace=None) -> torch.Tensor:
+    """forward with the tokens' experts and weights given (moe_lora_forward_topk): topk_ids [T][k]
+    int32 (-1: an empty slot) and topk_w [T][k] float32, as route returns them. With W1_scale
+    [E][2I] and W2_scale [E][h] (float32), W1 and W2 are uint8 E4M3 codes as in forward_fp8."""
+    d = dims_of(x, W1, A1)
+    T, h, I, E, nA, r = d.T, d.hidden, d.inter, d.n_experts, d.n_adapters, d.rank
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be a [T][k] tensor")
+    if (W1_scale is None) != (W2_scale is None):
+        raise ValueError("W1_scale and W2_scale go together")
+    k = topk_ids.shape[1]
+    dev, bf = x.get_device(), torch.bfloat16
+    wt = bf if W1_scale is None else torch.uint8
+    if y is None:
+        y = torch.empty((T, h), dtype=bf, device=x.device)
+    args = (_dense(x, "x", bf, (T, h), dev), _dense(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            _dense(topk_w, "topk_w", torch.float32, (T, k), dev), _dense(W1, "W1", wt, (E, 2 * I, h), dev),
+            _dense(W1_scale, "W1_scale", torch.float32, (E, 2 * I), dev), _dense(W2, "W2", wt, (E, h, I), dev),
+            _dense(W2_scale, "W2_scale", torch.float32, (E, h), dev), _dense(A1, "A1", bf, (nA, E, r, h), dev),
+            _dense(B1, "B1", bf, (nA, E, 2 * I, r), dev), _dense(A2, "A2", bf, (nA, E, r, I), dev),
+            _dense(B2, "B2", bf, (nA, E, h, r), dev), _dense(adapter_ids, "adapter_ids", torch.int32, (T,), dev))
+    if workspace is None:
+        workspace = new_workspace(d, k, x.device)
+    _on(dev, lib().moe_lora_forward_topk, "moe_lora_forward_topk", *args, k, ctypes.byref(d),
+        _dense(y, "y", bf, (T, h), dev), _dense(workspace, "workspace", torch.uint8, workspace.shape, dev),
+        workspace.numel())
+    return y
 
 
 def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y=None,

@@ -60,7 +60,7 @@ int resident_tiles() {
 // and the arrays go to the workspace. Returns the dynamic LDS bytes and fills the kernel's sizes.
 size_t align_lds_plan(int T, int k, int E, int nA, AlignArgs* a) {
   const size_t budget = (size_t)(kLdsBytes - kAlignStaticLds);
-  align_digits(E, nA, &a->digit_bits, &a->passes);
+  align_digits(E, nA, a->given_ids != 0, &a->digit_bits, &a->passes);
   a->seg_cap = align_seg_cap(T, k, E, nA);
   const size_t P = (size_t)T * k;
   const size_t counts = (size_t)(kAlignThreads / 64) << a->digit_bits;
@@ -443,12 +443,13 @@ int enqueue_forward(const ForwardPlan& pl, const MoeLoraLayout& L, const void* x
                     const void* W2, const void* A1, const void* B1, const void* A2, const void* B2,
                     const int32_t* adapter_ids, int32_t topk, const moe_lora_dims* d, void* y,
                     char* ws, hipStream_t stream, void* const* ev, const float* w1_scale,
-                    const float* w2_scale) {
+                    const float* w2_scale, const int32_t* given_ids = nullptr,
+                    const float* given_w = nullptr) {
   const bool fp8 = w1_scale != nullptr;
   const int T = d->T, h = d->hidden, I = d->inter, E = d->n_experts, nA = d->n_adapters, r = d->rank;
-  int* topk_ids = (int*)(ws + L.topk_ids);
-  float* topk_w = (float*)(ws + L.topk_w);
-  int* tok_flags = (int*)(ws + L.tok_flags);
+  const int* topk_ids = given_ids ? given_ids : (int*)(ws + L.topk_ids);
+  const float* topk_w = given_ids ? given_w : (float*)(ws + L.topk_w);
+  int* tok_flags = given_ids ? nullptr : (int*)(ws + L.tok_flags);
   int* sorted = (int*)(ws + L.sorted);
   int* n_blocks = (int*)(ws + L.n_blocks);
   int* block_expert = (int*)(ws + L.block_expert);
@@ -469,7 +470,8 @@ int enqueue_forward(const ForwardPlan& pl, const MoeLoraLayout& L, const void* x
   }
 
   if (!mark(ev, 0, stream)) return MOELORA_EHIP;
-  if (launch_route(router_logits, T, E, topk, topk_ids, topk_w, tok_flags, stream) != hipSuccess)
+  if (!given_ids && launch_route(router_logits, T, E, topk, (int*)(ws + L.topk_ids),
+                                 (float*)(ws + L.topk_w), tok_flags, stream) != hipSuccess)
     return MOELORA_EHIP;
   if (!mark(ev, 1, stream)) return MOELORA_EHIP;
 
@@ -496,6 +498,7 @@ int enqueue_forward(const ForwardPlan& pl, const MoeLoraLayout& L, const void* x
   al.sorted_ad = sorted_ad;
   al.n_blocks = n_blocks;
   al.g_lists = (int*)(ws + L.align_lists);
+  al.given_ids = given_ids ? 1 : 0;
   const size_t lds = align_lds_plan(T, topk, E, nA, &al);
   if (launch_align(al, lds, stream) != hipSuccess) return MOELORA_EHIP;
   if (!mark(ev, 2, stream)) return MOELORA_EHIP;
@@ -647,6 +650,7 @@ int enqueue_forward(const ForwardPlan& pl, const MoeLoraLayout& L, const void* x
   cb.part_cols = path.tc_dn.bn;
   cb.part_ncol = h / path.tc_dn.bn;
   cb.pair_row = pair_row;
+  cb.empty_slots = given_ids != nullptr;
   cb.topk_w = topk_w;
   cb.T = T;
   cb.k = topk;
@@ -684,6 +688,14 @@ int check_forward(const void* x, const float* router_logits, const void* W_route
   if (!in_scratch && ((uintptr_t)workspace & 255u) != 0) return MOELORA_EWORKSPACE;
   if (!in_scratch && workspace_bytes < L->total) return MOELORA_EWORKSPACE;
   return check_device();
+}
+
+// The sizes of a call with given choices: its align sorts one bucket more.
+int check_given_dims(const moe_lora_dims* d, int32_t topk) {
+  const int rc = validate_dims(d, topk);
+  if (rc != MOELORA_OK) return rc;
+  return (int64_t)d->n_experts * (d->n_adapters + 1) + 1 < ((int64_t)1 << 28) ? MOELORA_OK
+                                                                              : MOELORA_EINVAL_DIMS;
 }
 
 // The layer. W_router != nullptr: the router GEMM first writes the logits into the workspace
@@ -754,6 +766,29 @@ int moe_lora_forward_routed(const void* x, const void* W_router, const void* W1,
   }
   return forward_impl(x, nullptr, W_router, W1, W2, A1, B1, A2, B2, adapter_ids, topk, d, y,
                       workspace, workspace_bytes, stream, nullptr);
+}
+
+int moe_lora_forward_topk(const void* x, const int32_t* topk_ids, const float* topk_w, const void* W1,
+                          const float* W1_scale, const void* W2, const float* W2_scale,
+                          const void* A1, const void* B1, const void* A2, const void* B2,
+                          const int32_t* adapter_ids, int32_t topk, const moe_lora_dims* d, void* y,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_given_dims(d, topk);
+  if (rc != MOELORA_OK) return rc;
+  const bool fp8 = W1_scale || W2_scale;
+  ForwardPlan pl;
+  MoeLoraLayout L;
+  // (topk_w takes the place of the logits in the checks)
+  rc = check_forward(x, topk_w, nullptr, W1, W2, A1, B1, A2, B2, adapter_ids, topk, d, y, workspace,
+                     workspace_bytes, W1_scale, W2_scale, fp8, &pl, &L);
+  if (rc == MOELORA_OK || rc == MOELORA_EHIP || rc == MOELORA_EDEVICE) {
+    if (d->T > 0 && !topk_ids) return MOELORA_ENULL;
+    if (d->T > 0 && !aligned16(topk_ids)) return MOELORA_EALIGN;
+  }
+  if (rc != MOELORA_OK || d->T == 0) return rc;
+  return enqueue_forward(pl, L, x, nullptr, nullptr, W1, W2, A1, B1, A2, B2, adapter_ids, topk, d, y,
+                         (char*)workspace, (hipStream_t)stream, nullptr, W1_scale, W2_scale, topk_ids,
+                         topk_w);
 }
 
 int moe_lora_forward_fp8(const void* x, const float* router_logits, const void* W1q,

@@ -16,7 +16,8 @@ namespace moelora {
 // Each thread owns 16 consecutive features of one token: a slot's D row is read as four 16-byte
 // pieces per part, so the chain of dependent loads (pair row, part count, D) is paid once per
 // 64 bytes of each row.
-template <int MAXP>
+// EMPTY: slots may be empty (pair row -1): nothing is loaded for them and nothing added.
+template <int MAXP, bool EMPTY>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   constexpr int CH = 4;  // 4-feature chunks per thread
   const int h = a.h, k = a.k;
@@ -44,7 +45,9 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 #pragma unroll
   for (int j = 0; j < kMaxTopk; ++j)
     if (j < k)
-      np[j] = per_tile ? a.d_parts[(size_t)(rows[j] / a.part_rows) * a.part_ncol + ct] : a.ksplit;
+      np[j] = EMPTY && rows[j] < 0 ? 0
+              : per_tile ? a.d_parts[(size_t)(rows[j] / a.part_rows) * a.part_ncol + ct]
+                         : a.ksplit;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   constexpr int JS = 2;  // slots per batch of loads
 #pragma unroll
@@ -67,7 +70,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 #pragma unroll
     for (int jj = 0; jj < JS; ++jj) {
       const int j = j0 + jj;
-      if (j < k) {
+      if (j < k && !(EMPTY && rows[j] < 0)) {
 #pragma unroll
         for (int q = 0; q < CH; ++q) {
           f32x4 dv = d[jj][0][q];
@@ -98,14 +101,21 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
   if (a.d_parts && (a.part_rows <= 0 || a.part_cols <= 0 || a.part_cols % 16 != 0))
     return hipErrorInvalidValue;
   const dim3 grid((unsigned)((n + 255) / 256));
+  if (!a.d_parts && a.ksplit > 2) return hipErrorInvalidValue;
+#define MOELORA_COMBINE(MAXP_)                                                           \
+  do {                                                                                   \
+    if (a.empty_slots)                                                                   \
+      hipLaunchKernelGGL((combine_kernel<MAXP_, true>), grid, dim3(256), 0, stream, a);  \
+    else                                                                                 \
+      hipLaunchKernelGGL((combine_kernel<MAXP_, false>), grid, dim3(256), 0, stream, a); \
+  } while (0)
   if (a.d_parts)
-    hipLaunchKernelGGL(combine_kernel<kMaxParts>, grid, dim3(256), 0, stream, a);
+    MOELORA_COMBINE(kMaxParts);
   else if (a.ksplit == 1)
-    hipLaunchKernelGGL(combine_kernel<1>, grid, dim3(256), 0, stream, a);
-  else if (a.ksplit == 2)
-    hipLaunchKernelGGL(combine_kernel<2>, grid, dim3(256), 0, stream, a);
+    MOELORA_COMBINE(1);
   else
-    return hipErrorInvalidValue;
+    MOELORA_COMBINE(2);
+#undef MOELORA_COMBINE
   return hipGetLastError();
 }
 

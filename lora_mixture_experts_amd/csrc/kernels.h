@@ -31,12 +31,14 @@ struct AlignArgs {
   int digit_bits;  // radix digit width D (1..10)
   int passes;      // digits of the bucket key (passes * D >= its bit width)
   int seg_cap;     // min(T*k, E*(nA+1)) + 1: room for the segment starts (and deltas)
+  int given_ids = 0;  // 1: topk_ids come from the caller: a slot may be empty (-1; an id out of range
+                      // is flagged and taken as -1) and its pair is left out of the layout, pair_row -1
 };
 
-// Radix digits of the align kernel for E*(nA+1) buckets: as few passes of at most 10 bits as
-// the key width needs, the width spread evenly over them.
-inline void align_digits(int E, int nA, int* digit_bits, int* passes) {
-  const uint32_t nb = (uint32_t)E * (uint32_t)(nA + 1);
+// Radix digits of the align kernel for E*(nA+1) buckets (and one for empty slots): as few passes of
+// at most 10 bits as the key width needs, the width spread evenly over them.
+inline void align_digits(int E, int nA, bool given_ids, int* digit_bits, int* passes) {
+  const uint32_t nb = (uint32_t)E * (uint32_t)(nA + 1) + (given_ids ? 1u : 0u);
   int bits = 0;
   while (bits < 31 && (1u << bits) < nb) ++bits;
   if (bits < 1) bits = 1;
@@ -241,6 +243,7 @@ struct CombineArgs {
   const int* d_parts;
   int part_rows, part_cols, part_ncol;
   const int* pair_row;
+  bool empty_slots;  // pair_row may be -1: the slot adds nothing, its weight is not used
   const float* topk_w;
   int T, k, h;
   uint16_t* y;

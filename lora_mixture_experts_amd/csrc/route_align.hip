@@ -213,6 +213,8 @@ __global__ __launch_bounds__(256) void route_rank_kernel(const float* __restrict
 //            padded to block_m; segment table, expert offsets, row block -> segment table
 //   phase 3  padding slots (-1), row block -> expert table; pair ids (and their adapters)
 //            into their padded rows
+// Ids given by the caller may leave slots empty: their pairs take a bucket past all others, so
+// they sort behind the live ones, and phases 1 to 3 see the live ones only.
 // Every step is a flat loop over pairs, segments or experts: the work is O(T*k + E) whatever
 // the number of adapters. The arrays live in LDS when they fit and in the workspace otherwise.
 // ------------------------------------------------------------------------------------------
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
 
   // phase 0
   // (loads in batches of 8 per thread, issued before any is used)
-  int fl_nonfinite = 0, fl_range = 0;
+  int fl_nonfinite = 0, fl_range = 0, fl_expert = 0, n_empty = 0;
   for (int t0 = 0; a.tok_flags && t0 < T; t0 += 8 * bd) {
     int f[8];
 #pragma unroll
@@ -328,6 +330,12 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
         fl_range = 1;
         av[u] = -1;
       }
+      if (a.given_ids && p < P && (ex[u] < 0 || ex[u] >= E)) {
+        fl_expert |= ex[u] != -1;
+        ++n_empty;
+        key[p] = E * nb1;
+        continue;
+      }
       if (p < P) key[p] = ex[u] * nb1 + av[u] + 1;
     }
   }
@@ -337,6 +345,13 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
   }
   fl_nonfinite = __syncthreads_or(fl_nonfinite);
   fl_range = __syncthreads_or(fl_range);
+  int PL = P;  // pairs of the layout
+  if (a.given_ids) {
+    fl_expert = __syncthreads_or(fl_expert);
+    int d0, d1, d2, empty;
+    block_excl_scan2(n_empty, 0, d0, d1, empty, d2, s_red);
+    PL = P - empty;
+  }
 
   // radix passes, least significant digit first; pass 0 reads the pairs in pair order
   const int D = a.digit_bits, dmask = (1 << D) - 1, ncnt = nwaves << D;
@@ -396,8 +411,8 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
   // phase 1: contiguous ranges of sorted positions per thread
   int nseg;
   {
-    const int per_t = (P + bd - 1) / bd;
-    const int lo = min(P, tid * per_t), hi = min(P, lo + per_t);
+    const int per_t = (PL + bd - 1) / bd;
+    const int lo = min(PL, tid * per_t), hi = min(PL, lo + per_t);
     const int prev0 = lo > 0 ? key[sorted[lo - 1]] : -1;
     int prev = prev0, ns = 0;
     for (int i = lo; i < hi; ++i) {
@@ -415,7 +430,7 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
       prev = kk;
       sid[i] = sg;
     }
-    if (tid == 0) seg_lo[nseg] = P;
+    if (tid == 0) seg_lo[nseg] = PL;
   }
   __syncthreads();
 
@@ -476,7 +491,7 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
   for (int e = tid; e <= E; e += bd) a.expert_offsets[e] = s_off[e];
   if (tid == 0) {
     *a.n_seg = nseg;
-    *a.flags = (fl_nonfinite ? 1 : 0) | (fl_range ? 2 : 0);
+    *a.flags = (fl_nonfinite ? 1 : 0) | (fl_range ? 2 : 0) | (fl_expert ? 4 : 0);
     if (a.n_blocks) *a.n_blocks = s_off[E] / block_m;
   }
   __syncthreads();
@@ -505,6 +520,10 @@ __global__ __launch_bounds__(1024) void align_kernel(AlignArgs a) {
   }
   for (int i = tid; i < P; i += bd) {
     const int p = sorted[i];
+    if (i >= PL) {  // an empty slot
+      if (a.pair_row) a.pair_row[p] = -1;
+      continue;
+    }
     const int pos = i + delta[sid[i]];
     a.sorted_pairs[pos] = p;
     if (a.pair_row) a.pair_row[p] = pos;
