@@ -3,8 +3,9 @@
 Thin ctypes binding over libmoelora.so (include/moelora.h). Every step of the layer runs in
 the library's HIP kernels; this module only checks tensor shapes, allocates outputs and the
 workspace with torch when the caller does not pass them, and hands raw device pointers and
-torch's current HIP stream to the C ABI. There is no fallback: without the built library or
-a gfx950 device every call raises.
+torch's current HIP stream to the C ABI. For route and linear, whose kernels take a few
+microseconds, a compiled module (csrc/binding.cpp) does the same. There is no fallback: without
+the built library or a gfx950 device every call raises.
 """
 from __future__ import annotations
 
@@ -66,6 +67,7 @@ GROUP_SCORES = {"max": 0, "top2": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 
 _lib = None
+_compiled = None
 
 
 def lib() -> ctypes.CDLL:
@@ -122,6 +124,20 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_debug_status.restype = ctypes.c_int
         _lib = L
     return _lib
+
+
+def _native():
+    """The compiled half of the binding (raises if it has not been built)."""
+    global _compiled
+    if _compiled is None:
+        lib()  # (its message, if the library is missing)
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so is missing or does not load ({e}): build it with "
+                               "lora_mixture_experts_amd.build.build()") from e
+        _compiled = _binding
+    return _compiled
 
 
 def strerror(code: int) -> str:
@@ -345,42 +361,14 @@ def sgmv(x, A, B, adapter_ids, y, workspace=None) -> torch.Tensor:
     return y
 
 
-def _refuse(t, name: str, dtype, shape, device: int):
-    """Raises for a tensor that a fast check did not take."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
-    raise ValueError(f"{name}: its rows must be dense and must not overlap")
-
-
-def _dense(t, name: str, dtype, shape, device: int) -> int:
-    """Pointer of a contiguous tensor on GPU `device`, None for None. (These checks run on every call
-    of an operator that takes a few microseconds: they are kept to a few attribute reads.)"""
+def _dense(t, name: str, dtype, shape, device: int):
+    """Pointer of a contiguous tensor on GPU `device`, None for None."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == device >= 0 and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, device)
+    _expect(t, name, dtype, shape)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{device}")
     return t.data_ptr()
-
-
-def _rows(t, name: str, dtype, shape, device: int):
-    """Pointer and row stride of a matrix on GPU `device` whose rows are dense but may lie apart."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device >= 0:
-        row, col = t.stride()
-        if col == 1 or shape[1] <= 1:
-            if shape[0] <= 1:  # (the stride of a single row means nothing)
-                return t.data_ptr(), max(row, shape[1])
-            if row >= shape[1]:
-                return t.data_ptr(), row
-    _refuse(t, name, dtype, shape, device)
 
 
 def _on(device: int, call, what: str, *args):
@@ -405,27 +393,16 @@ def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: i
     chosen from; renormalize: weights over the sum of the chosen; token_mask [T] bool: False for
     rows of padding. Empty slots hold expert -1 and weight 0. token_flags [T] int32, when given,
     receives 1 where a token's logits were not all finite."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise ValueError("logits must be a [T][E] tensor")
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {sorted(SCORINGS)}")
     if group_score not in GROUP_SCORES:
         raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}")
-    T, E = logits.shape
-    dev = logits.get_device()
-    lp, stride = _rows(logits, "logits", torch.float32, (T, E), dev)
-    if topk_ids is None:
-        topk_ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = logits.new_empty((T, max(topk, 0)))
-    r = Router(T, E, topk, SCORINGS[scoring], n_groups, topk_groups, GROUP_SCORES[group_score],
-               1 if renormalize else 0, scale, stride)
-    _on(dev, lib().moe_lora_route, "moe_lora_route", lp, _dense(bias, "bias", torch.float32, (E,), dev),
-        _dense(token_mask, "token_mask", torch.bool, (T,), dev), ctypes.byref(r),
-        _dense(topk_ids, "topk_ids", torch.int32, (T, max(topk, 0)), dev),
-        _dense(topk_w, "topk_w", torch.float32, (T, max(topk, 0)), dev),
-        _dense(token_flags, "token_flags", torch.int32, (T,), dev))
-    return topk_ids, topk_w
+    out = (_compiled or _native()).route(logits, topk, SCORINGS[scoring], bias, n_groups, topk_groups,
+                                         GROUP_SCORES[group_score], 1 if renormalize else 0, scale, token_mask,
+                                         topk_ids, topk_w, token_flags)
+    if type(out) is int:
+        raise MoeLoraError(out, "moe_lora_route")
+    return out
 
 
 def forward_topk(x, topk_ids, topk_w, W1, W2, A1, B1, A2, B2, adapter_ids, *, W1_scale=None, W2_scale=None,
@@ -467,36 +444,12 @@ def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y
     W (w_scale, bias) has 2 N rows, gate then up. Rows of x, W, residual and y may lie apart (x
     and W rows 16-byte aligned). y may be the residual. sgmv(x, A, B, adapter_ids, y) adds a
     batch's adapters to a projection without an activation."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
-        raise ValueError("x must be [T][K] and W [N][K]")
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
-    T, K = x.shape
-    rows = W.shape[0]
-    N = rows
-    if act == "swiglu":
-        if rows % 2:
-            raise ValueError("W of swiglu has gate and up rows: an even number")
-        N = rows // 2
-    bf = torch.bfloat16
-    dev = x.get_device()
-    xp, xs = _rows(x, "x", bf, (T, K), dev)
-    wp, ws = _rows(W, "W", bf if w_scale is None else torch.uint8, (rows, K), dev)
-    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", bf, (T, N), dev)
-    if y is None:
-        y = x.new_empty((T, N))
-    yp, ys = _rows(y, "y", bf, (T, N), dev)
-    d = LinearDims(T, K, N, ACTIVATIONS[act], 0 if w_scale is None else 1, xs, ws, ys, rs)
-    L, dp = lib(), ctypes.byref(d)
-    if workspace is None:
-        need = L.moe_lora_linear_workspace_size(dp)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    kp, kb = (None, 0) if workspace is None else (
-        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel())
-    _on(dev, L.moe_lora_linear, "moe_lora_linear", xp, wp, _dense(w_scale, "w_scale", torch.float32, (rows,), dev),
-        _dense(bias, "bias", bf, (rows,), dev), rp, dp, yp, kp, kb)
-    return y
+    out = (_compiled or _native()).linear(x, W, w_scale, bias, ACTIVATIONS[act], residual, y, workspace)
+    if type(out) is int:
+        raise MoeLoraError(out, "moe_lora_linear")
+    return out
 
 
 def forward_fp8(x, router_logits, W1q, W1_scale, W2q, W2_scale, A1, B1, A2, B2, adapter_ids,

@@ -1,4 +1,5 @@
-"""Build libmoelora.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree."""
+"""Build libmoelora.so (HIP kernels + C ABI) for gfx950 with hipcc, and the compiled half of the
+Python binding (_binding.so, host code only, on torch's headers) with g++, in-tree."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -6,6 +7,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoelora.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -33,20 +36,40 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """csrc/binding.cpp against torch and the library just linked."""
+    import torch
+    from torch.utils import cpp_extension
+
+    includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_path("include"), "/opt/rocm/include"]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-I" + i for i in includes],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_hip", LIB, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link the shared library. Always recompiles."""
+    """Compile every HIP source and link the shared library and the binding. Always recompiles."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmoelora.so", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     if verbose:
         print(f"built {LIB}")
+        print(f"built {BINDING}")
     return LIB
 
 
