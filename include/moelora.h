@@ -286,7 +286,7 @@ typedef struct {
   int32_t group_score;        /* MOELORA_GROUP_* */
   int32_t renormalize;        /* 0 or 1 */
   float scale;                /* finite */
-  int64_t logits_stride;      /* floats between two tokens' logits, >= n_experts */
+  int64_t logits_stride;      /* floats between two tokens' logits, in [n_experts, 2^22) */
 } moe_lora_router;
 
 /* Chooses experts by `r` (above). logits f32 [T] rows of n_experts, bias f32 [n_experts] or NULL,

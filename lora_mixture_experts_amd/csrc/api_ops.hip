@@ -12,6 +12,8 @@ using namespace moelora;
 
 namespace {
 
+constexpr int64_t kMaxRowStride = (int64_t)1 << 22;  // a workgroup's (up to 256) rows stay under 2 GiB
+
 int validate_router(const moe_lora_router* r) {
   if (!r) return MOELORA_ENULL;
   if (r->T < 0 || r->T >= (1 << 26) || r->n_experts < 1 || r->n_experts > kMaxExperts) return MOELORA_EINVAL_DIMS;
@@ -26,12 +28,10 @@ int validate_router(const moe_lora_router* r) {
     return MOELORA_EINVAL_DIMS;
   if (r->renormalize != 0 && r->renormalize != 1) return MOELORA_EINVAL_DIMS;
   if (!std::isfinite(r->scale)) return MOELORA_EINVAL_DIMS;
-  if (r->logits_stride < r->n_experts || r->logits_stride >= ((int64_t)1 << 31))
+  if (r->logits_stride < r->n_experts || r->logits_stride >= kMaxRowStride)
     return MOELORA_EINVAL_DIMS;
   return MOELORA_OK;
 }
-
-constexpr int64_t kMaxRowStride = (int64_t)1 << 22;  // 256 rows of a tile stay under 2 GiB
 
 int validate_linear(const moe_lora_linear_dims* d, bool residual) {
   if (!d) return MOELORA_ENULL;

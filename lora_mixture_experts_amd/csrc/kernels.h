@@ -88,7 +88,7 @@ struct RouteScoredArgs {
   int* topk_ids;     // [T][k], -1 for an empty slot
   float* topk_w;     // [T][k], 0 for an empty slot
   int* token_flags;  // [T] or nullptr: 1 where a logit of the row was not finite
-  int Gp, vec;       // (launcher) G rounded up to a power of two; rows and groups load 16 bytes
+  int log_gp, vec;   // (launcher) log2 of G rounded up to a power of two; rows and groups load 16 bytes
 };
 
 // LoRA shrink z = X A^T for the rows of the sorted layout.

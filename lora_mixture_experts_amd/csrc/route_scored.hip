@@ -12,11 +12,15 @@
 // Mapping: L lanes (16 or a whole wavefront) hold one token, V experts a lane, each group on
 // lanes of its own. A choice is one double: the value with its lowest 10 mantissa bits replaced by
 // the expert id (so that a larger key is a larger value or, on a tie, a lower id), and
-// v_max_f64 / v_min_f64 order value and id in two instructions. A float logit is exact in the
-// remaining 42 bits; scores are computed in double, so that two experts are told apart at 2^-42
-// of their choice values, not at a float's rounding of an exponential. Each lane sorts its V
-// keys (Batcher's odd-even merge network), then log2 L exchanges merge the best K of two lanes:
-// the larger of a[i] and b[K-1-i] are the K largest of both and form a bitonic sequence.
+// v_max_f64 / v_min_f64 order value and id in two instructions. Each lane sorts its V keys
+// (Batcher's odd-even merge network), then log2 L exchanges merge the best K of two lanes: the
+// larger of a[i] and b[K-1-i] are the K largest of both and form a bitonic sequence.
+//
+// A float logit is exact in a key. Choice values made of scores have to be told apart at 2^-42 of
+// their size, not at a float's rounding of an exponential, but hardly ever need it: they are
+// computed in fp32 first, and only where two neighbours of the result, the last one chosen and the
+// best one left, or the last group kept and the first one dropped, lie closer than the fp32 error
+// bound does the wavefront choose again from scores in double.
 #include "common.h"
 #include "kernels.h"
 
@@ -24,7 +28,9 @@ namespace moelora {
 
 namespace {
 
-constexpr double kNone = -1.7e308;  // key of an expert that cannot be chosen
+constexpr double kNone = -1e300;  // value of an expert that cannot be chosen
+constexpr double kLeast = -1e299;  // keys above it can be
+constexpr float kBig = 3.4e38f;
 
 __device__ __forceinline__ double max64(double a, double b) {
   double r;  // (keys are never NaN: no canonicalising copies)
@@ -81,6 +87,13 @@ __device__ __forceinline__ double exp64(double x) {
 __device__ __forceinline__ double rcp64(double x) {
   const double r = __builtin_amdgcn_rcp(x);
   return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+}
+
+// e^x in fp32 to about 2^-22: the hardware's 2^t, with what t = x log2(e) lost to rounding put back.
+__device__ __forceinline__ float exp32(float x) {
+  const float t = x * 1.44269504f;
+  const float lost = __builtin_fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
+  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(lost, 0.693147181f, 1.f);
 }
 
 template <int CTRL>
@@ -152,6 +165,14 @@ __device__ __forceinline__ void clean(double* a) {
       if ((i & s) == 0) order(a[i], a[i + s]);
 }
 
+// a[0..N) becomes the N best of two falling lists.
+template <int N>
+__device__ __forceinline__ void merge_best(double* a, const double* b) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = max64(a[i], b[N - 1 - i]);
+  clean<N>(a);
+}
+
 // The exchange steps from I on: each lane's `list` (LEN keys in falling order) becomes the best
 // min(2 LEN, KP) of its own and its partner's.
 template <int L, int KP, int LEN, int I>
@@ -165,111 +186,127 @@ __device__ __forceinline__ void merge_lanes(double* list) {
     } else {
       double b[KP];
 #pragma unroll
-      for (int i = 0; i < KP; ++i) b[i] = partner<I>(list[KP - 1 - i]);
-#pragma unroll
-      for (int i = 0; i < KP; ++i) list[i] = max64(list[i], b[i]);
-      clean<KP>(list);
+      for (int i = 0; i < KP; ++i) b[i] = partner<I>(list[i]);
+      merge_best<KP>(list, b);
       merge_lanes<L, KP, KP, I + 1>(list);
     }
   }
 }
 
-// Groups h = 1 .. 15 rows further round, by row rotations (an immediate each).
-template <int N>
-__device__ __forceinline__ int beaten_by(double mine, int step, int count) {
-  if constexpr (N < 16) {
-    if (N % step == 0) count += dpp64<0x120 + N>(mine) > mine ? 1 : 0;
-    return beaten_by<N + 1>(mine, step, count);
-  } else {
-    return count;
-  }
+// Groups of LG lanes, L = 16: how many of the others beat this one (row rotations by LG, 2 LG, ...).
+template <int LG, int N>
+__device__ __forceinline__ int beaten_by(double mine, int count) {
+  if constexpr (N < 16) return beaten_by<LG, N + LG>(mine, count + (dpp64<0x120 + N>(mine) > mine ? 1 : 0));
+  else return count;
 }
 
-}  // namespace
+enum { kByLogit, kByScore32, kByScore64 };
 
-// L lanes a token, V experts a lane, lists of KP >= min(k, experts of a token's lanes).
-template <int L, int V, int KP>
-__global__ __launch_bounds__(256) void route_scored_kernel(RouteScoredArgs a) {
-  constexpr int TPB = 256 / L;
-  const int tl = threadIdx.x % L;
-  const int t = blockIdx.x * TPB + threadIdx.x / L;
-  // (no early exit: every lane takes part in the exchanges)
-  const bool active = t < a.T && (!a.token_mask || a.token_mask[t < a.T ? t : 0] != 0);
-  const int Lg = L / a.Gp, g = tl / Lg, gl = tl % Lg;
-  const int S = a.S;
-  const float* row = a.logits + (size_t)(t < a.T ? t : 0) * a.ld + g * S;
-  const bool group_lane = active && g < a.G;
-
-  // The lane's experts are chunks of W, the chunks of a group dealt to its lanes in turn.
-  auto local = [&](int j) { return a.vec ? ((j / 4) * Lg + gl) * 4 + j % 4 : j * Lg + gl; };
-  float l[V], b[V];
-  const float* brow = a.bias ? a.bias + g * S : nullptr;
-  if (V % 4 == 0 && a.vec) {
-#pragma unroll
-    for (int j = 0; j < V / 4 * 4; j += 4) {
-      f32x4 v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, vb = {0.f, 0.f, 0.f, 0.f};
-      if (group_lane && local(j) < S) {
-        v = *reinterpret_cast<const f32x4*>(row + local(j));
-        if (brow) vb = *reinterpret_cast<const f32x4*>(brow + local(j));
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        l[(j + c) % V] = v[c];
-        b[(j + c) % V] = vb[c];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool have = group_lane && local(j) < S;
-      l[j] = have ? row[local(j)] : -INFINITY;
-      b[j] = have && brow ? brow[local(j)] : 0.f;
-    }
+// The experts of a lane, in V values: chunks of 4 consecutive ones where rows and groups are 16-byte
+// aligned (of 4 that lie Lg apart else), the chunks of a group dealt to its Lg lanes in turn.
+template <int V>
+struct LaneExperts {
+  int g, Lg;               // the lane's group, lanes of a group
+  int first, chunk, next;  // id of value 0; between chunks; between the values of a chunk
+  bool vec, full;          // 16-byte loads; every value of every lane is an expert
+  float b[V];              // biases: 0 without, NaN (never chosen) where not finite
+  __device__ __forceinline__ int id(int j) const { return first + j / 4 * chunk + j % 4 * next; }
+  __device__ __forceinline__ bool inside(const RouteScoredArgs& a, int j) const {
+    return g < a.G && id(j) < (g + 1) * a.S;
   }
-  bool bad = false;
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const bool fin = __builtin_isfinite(l[j]);
-    bad |= !fin && group_lane && local(j) < S;
-    l[j] = fin ? l[j] : -INFINITY;
-    top = fmaxf(top, l[j]);
-  }
-  const bool softmax = a.scoring == 0;
-  if (softmax) top = over_lanes<L, 0>(top, [](float x, float y) { return fmaxf(x, y); });
 
-  // choice values and keys
-  double key[V < KP ? KP : V];
-  const bool by_score = a.by_score != 0;
-  if (by_score) {
-    double c[V];
-    if (softmax) {
-      double z = 0.0;
+  __device__ __forceinline__ LaneExperts(const RouteScoredArgs& a, int tl, int L) {
+    const int log_lg = __builtin_ctz(L) - a.log_gp;
+    Lg = 1 << log_lg;
+    g = tl >> log_lg;
+    vec = V % 4 == 0 && a.vec;
+    full = a.G == (1 << a.log_gp) && a.S == Lg * V;
+    chunk = 4 * Lg;
+    next = vec ? 1 : Lg;
+    first = g * a.S + (tl & (Lg - 1)) * (vec ? 4 : 1);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.bias, a.bias ? (uint32_t)(a.G * a.S) * 4 : 0u);
+    load(r, 0u, b, [](int) { return true; });
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        c[j] = l[j] > -INFINITY ? exp64((double)l[j] - (double)top) : 0.0;
-        z += c[j];
+    for (int j = 0; j < V; ++j) b[j] = __builtin_isfinite(b[j]) ? b[j] : __builtin_nanf("");
+  }
+
+  // The lane's values of a row of floats at byte offset `row` of r: offsets out of range load zero and
+  // no memory.
+  template <class Have>
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row, float* v, Have have) const {
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < V / 4 * 4; j += 4) {
+        const u32x4 q = bufld16(r, have(j) ? row + (uint32_t)id(j) * 4 : kOutOfRange);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[(j + c) % V] = __uint_as_float(q[c]);
       }
-      z = over_lanes<L, 0>(z, [](double x, double y) { return x + y; });
-      const double inv = rcp64(z > 0.0 ? z : 1.0);
-#pragma unroll
-      for (int j = 0; j < V; ++j) c[j] *= inv;
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) c[j] = rcp64(1.0 + exp64(fmin(-(double)l[j], 700.0)));
+      for (int j = 0; j < V; ++j)
+        v[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            r, (int)(have(j) ? row + (uint32_t)id(j) * 4 : kOutOfRange), 0, 0));
+    }
+  }
+};
+
+// 1/x to a unit in the last place.
+__device__ __forceinline__ float rcp32(float x) { return __builtin_amdgcn_rcpf(x); }
+
+__device__ __forceinline__ float most(float p, float q) { return fmaxf(p, q); }
+__device__ __forceinline__ float add(float p, float q) { return p + q; }
+
+// The largest finite logit of a token.
+template <int L, int V>
+__device__ __forceinline__ float largest(const float* l) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < V; ++j) top = fmaxf(top, __builtin_isfinite(l[j]) ? l[j] : -INFINITY);
+  return fmaxf(over_lanes<L, 0>(top, most), -kBig);  // (no expert at all: finite)
+}
+
+// The LIST = min(V, KP) best keys of the lane's experts, falling, in key[0..LIST). l: the logits (not
+// finite: not eligible). kByScore32: c32 the choice values (NaN or -infinity for none), unsure where
+// the bound does not settle the groups.
+template <int MODE, bool SOFTMAX, int L, int V, int KP>
+__device__ __forceinline__ void lane_list(const RouteScoredArgs& a, const LaneExperts<V>& x, const float* l,
+                                          float top, double* key, float* c32, bool& unsure) {
+  if constexpr (MODE == kByLogit) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)  // (l * 0 is NaN where l is not finite, and max takes the other side)
+      key[j] = with_id<10>(max64((double)__builtin_fmaf(l[j], 0.f, l[j] + 0.f), kNone), x.id(j));
+  } else {
+    double inv = 1.0;
+    if (SOFTMAX) {
+      double z = 0.0;  // (in double: its rounding would scale every score)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = __builtin_isfinite(l[j]);
+        if (MODE == kByScore64) z += exp64(in ? (double)l[j] - (double)top : -1000.0);
+        else z += (double)exp32(in ? fmaxf(l[j] - top, -200.f) : -200.f);
+      }
+      z = over_lanes<L, 0>(z, [](double p, double q) { return p + q; });
+      inv = rcp64(max64(z, 1e-300));
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const bool ok = l[j] > -INFINITY && __builtin_isfinite(b[j]);
-      key[j] = ok ? with_id<10>(c[j] + (double)b[j], g * S + local(j)) : kNone;
+      double c;
+      if constexpr (MODE == kByScore32) {
+        const float s = SOFTMAX ? exp32(fmaxf(l[j] - top, -200.f)) * (float)inv
+                                : __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -1.44269504f));
+        c32[j] = __builtin_fmaf(l[j], 0.f, s + x.b[j]);
+        c = (double)c32[j];
+      } else {
+        const double v = max64((double)l[j], -700.0);
+        const double s = SOFTMAX ? exp64(v - (double)top) * inv : rcp64(1.0 + exp64(-v));
+        c = s + (double)__builtin_fmaf(l[j], 0.f, x.b[j]);
+      }
+      key[j] = with_id<10>(max64(c, kNone), x.id(j));
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      key[j] = l[j] > -INFINITY ? with_id<10>((double)(l[j] + 0.f), g * S + local(j)) : kNone;
   }
 
-  if (a.Gp > 1 && a.topk_groups < a.G) {
+  bool kept = true;
+  if (a.topk_groups < a.G) {
     // group scores: the two largest keys of the group, over the lane's experts, then over the
     // group's lanes
     double m1 = kNone, m2 = kNone;
@@ -282,90 +319,169 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteScoredArgs a) {
       m2 = max64(min64(m1, o1), max64(m2, o2));
       m1 = max64(m1, o1);
     };
+    const int Lg = x.Lg;
     if (Lg > 1) join(partner<0>(m1), partner<0>(m2));
     if (Lg > 2) join(partner<1>(m1), partner<1>(m2));
     if (Lg > 4) join(partner<2>(m1), partner<2>(m2));
     if (Lg > 8) join(partner<3>(m1), partner<3>(m2));
     if constexpr (L == 64)
       if (Lg > 16) join(partner<4>(m1), partner<4>(m2));
-    double gs = kNone;
-    if (m1 > kNone) {
-      double v = without_id(m1);
-      if (a.group_top2 && m2 > kNone) v += without_id(m2);
-      gs = with_id<10>(v, g);
-    }
+    const double second = a.group_top2 && m2 > kLeast ? without_id(m2) : 0.0;
+    const double gs = with_id<10>(max64(without_id(m1) + second, kNone), x.g);
     int rank = 0;  // groups that beat this one
     if constexpr (L == 16) {
-      rank = beaten_by<1>(gs, Lg, 0);
+      if (Lg == 1) rank = beaten_by<1, 1>(gs, 0);
+      else if (Lg == 2) rank = beaten_by<2, 2>(gs, 0);
+      else if (Lg == 4) rank = beaten_by<4, 4>(gs, 0);
+      else rank = beaten_by<8, 8>(gs, 0);
     } else {
-      const int base = (threadIdx.x & 63) - tl;
-      for (int h = 0; h < a.G; ++h) rank += __shfl(gs, base + h * Lg) > gs ? 1 : 0;
+      for (int h = 0; h < a.G; ++h) rank += __shfl(gs, h * Lg) > gs ? 1 : 0;
     }
-    if (rank >= a.topk_groups) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = kNone;
+    kept = rank < a.topk_groups;
+    if constexpr (MODE == kByScore32) {
+      const float gf = (float)gs;
+      const float last = over_lanes<L, 0>(rank == a.topk_groups - 1 ? gf : -kBig, most);
+      const float next = over_lanes<L, 0>(rank == a.topk_groups ? gf : -kBig, most);
+      // twice an fp32 choice's error for each of up to two summands
+      unsure |= gs > kLeast && next > -1e38f && last - next < 0x1p-18f + 0x1p-20f * fabsf(last);
     }
   }
 
-  // the KP best of the lane, then of the token
   if constexpr (V <= KP) {
     sort_keys<V>(key);
-    merge_lanes<L, KP, V, 0>(key);
   } else {
 #pragma unroll
     for (int j = 0; j < V; j += KP) sort_keys<KP>(key + j);
 #pragma unroll
-    for (int j = KP; j < V; j += KP) {
+    for (int j = KP; j < V; j += KP) merge_best<KP>(key, key + j);
+  }
+  constexpr int LIST = V < KP ? V : KP;
 #pragma unroll
-      for (int i = 0; i < KP; ++i) key[i] = max64(key[i], key[j + KP - 1 - i]);
-      clean<KP>(key);
+  for (int i = 0; i < LIST; ++i) key[i] = kept ? key[i] : kNone;
+  if constexpr (MODE == kByScore32) {
+    if (!kept)
+#pragma unroll
+      for (int j = 0; j < V; ++j) c32[j] = -INFINITY;
+  }
+}
+
+// Twice the error of an fp32 choice value, the bound for a difference: under 2^-21 of its score (at
+// most 1) and half a unit of its sum.
+__device__ __forceinline__ float choice_error(float c) { return 0x1p-19f + 0x1p-21f * fabsf(c); }
+
+// What the weights need of a token: the softmax's largest logit and sum over the row.
+struct RowSums {
+  float top, z;
+};
+
+template <int L, int V>
+__device__ __forceinline__ RowSums row_sums(const RouteScoredArgs& a, const float* l, float top) {
+  RowSums r{top, 1.f};
+  if (a.scoring == 0 && !a.renormalize) {
+    float z = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) z += __builtin_isfinite(l[j]) ? exp32(fmaxf(l[j] - top, -200.f)) : 0.f;
+    r.z = over_lanes<L, 0>(z, add);
+  }
+  return r;
+}
+
+// Largest value that the renormalised weights of a token are taken relative to, per chosen logit.
+__device__ __forceinline__ float exponent_of(const RouteScoredArgs& a, bool live, float lv) {
+  return !live ? -INFINITY : a.scoring == 0 ? lv : fminf(lv, 0.f);
+}
+
+// Weight of a chosen logit before the division by the sum. Softmax: e^(l - m), m the largest chosen
+// logit (or the row's, where the weights are not renormalised). Sigmoid: e^min(l,0) / (1 + e^-|l|);
+// renormalised, the common factor e^m of the largest min(l, 0) is left out of all, so that scores
+// which are all tiny keep their ratios.
+__device__ __forceinline__ float weight_of(const RouteScoredArgs& a, bool live, float lv, float m, RowSums r) {
+  if (!live) return 0.f;
+  if (a.scoring == 0) return a.renormalize ? exp32(fmaxf(lv - m, -200.f)) : exp32(fmaxf(lv - r.top, -200.f)) * rcp32(r.z);
+  return exp32(fmaxf(fminf(lv, 0.f) - (a.renormalize ? m : 0.f), -200.f)) *
+         rcp32(1.f + exp32(fmaxf(-fabsf(lv), -200.f)));
+}
+
+}  // namespace
+
+// L lanes a token, V experts a lane, lists of KP >= min(k, experts of a token's lanes). (4 wavefronts a
+// SIMD asked for where 129 registers would leave 3: 33.6 -> 31.1 us for 65536 tokens of 256 experts)
+template <int L, int V, int KP>
+__global__ __launch_bounds__(256, V == 16 && KP == 8 ? 4 : 1) void route_scored_kernel(RouteScoredArgs a) {
+  constexpr int TPB = 256 / L;
+  const int tl = threadIdx.x % L;
+  const int t = blockIdx.x * TPB + threadIdx.x / L;
+  // (no early exit: every lane takes part in the exchanges)
+  const bool active = t < a.T && (!a.token_mask || a.token_mask[t < a.T ? t : 0] != 0);
+  const LaneExperts<V> x(a, tl, L);
+  float l[V];
+  x.load(make_rsrc(a.logits + (size_t)blockIdx.x * TPB * a.ld, 0x7fffffffu),
+         (uint32_t)(threadIdx.x / L) * (uint32_t)a.ld * 4, l,
+         [&](int j) { return active && x.inside(a, j); });
+  if (a.token_flags) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) bad |= !__builtin_isfinite(l[j]);
+    const float any = over_lanes<L, 0>(bad ? 1.f : 0.f, most);
+    if (t < a.T && tl == 0) a.token_flags[t] = any != 0.f ? 1 : 0;
+  }
+  if (!x.full) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = x.inside(a, j) ? l[j] : -INFINITY;
+  }
+  const bool softmax = a.scoring == 0;
+  const float top = softmax ? largest<L, V>(l) : 0.f;
+
+  // the choice: lane i < k gets slot i's key
+  bool unsure = false;
+  auto choose = [&](auto mode, auto soft) {
+    constexpr int MODE = decltype(mode)::value;
+    double key[V < KP ? KP : V];
+    float c32[V];
+    lane_list<MODE, decltype(soft)::value, L, V, KP>(a, x, l, top, key, c32, unsure);
+    merge_lanes<L, KP, (V < KP ? V : KP), 0>(key);
+    double mine = kNone;
+#pragma unroll
+    for (int i = 0; i < KP; ++i) mine = tl == i ? key[i] : mine;
+    if (tl >= a.k) mine = kNone;
+    if constexpr (MODE == kByScore32) {
+      // each slot against the next one, and how many experts come as near as that to the last
+      const float c = (float)mine, next = dpp32<0x101>(c);  // row_shl 1: lane i + 1's
+      const bool live = mine > kLeast;
+      unsure |= tl + 1 < a.k && live && next > -1e38f && c - next < choice_error(c);
+      const float near = __shfl(live ? c - choice_error(c) : kBig, ((threadIdx.x & 63) / L) * L + a.k - 1);
+      float count = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) count += c32[j] >= near ? 1.f : 0.f;
+      unsure |= over_lanes<L, 0>(count, add) > (float)a.k;
     }
-    merge_lanes<L, KP, KP, 0>(key);
+    return mine;
+  };
+  using std::integral_constant;
+  double mine;
+  if (!a.by_score) {
+    mine = choose(integral_constant<int, kByLogit>{}, std::false_type{});
+  } else if (softmax) {
+    mine = choose(integral_constant<int, kByScore32>{}, std::true_type{});
+    if (__ballot(unsure && active)) mine = choose(integral_constant<int, kByScore64>{}, std::true_type{});
+  } else {
+    mine = choose(integral_constant<int, kByScore32>{}, std::false_type{});
+    if (__ballot(unsure && active)) mine = choose(integral_constant<int, kByScore64>{}, std::false_type{});
   }
 
-  // lane i < k of the token takes slot i
-  constexpr int LIST = V * L < KP ? V * L : KP;  // keys the token's lanes can hold
-  double mine = kNone;
-#pragma unroll
-  for (int i = 0; i < LIST; ++i) mine = tl == i ? key[i] : mine;
-  const bool live = active && tl < a.k && mine > kNone;
+  const bool live = active && mine > kLeast;
   const int e = live ? id_of(mine) : -1;
   float lv = 0.f;
-  if (live) lv = by_score ? a.logits[(size_t)t * a.ld + e] : (float)without_id(mine);
-  float w = 0.f;
-  auto add = [](float x, float y) { return x + y; };
-  auto most = [](float x, float y) { return fmaxf(x, y); };
-  if (softmax) {
-    if (a.renormalize) {
-      // over the chosen alone: their largest logit in the place of the row's
-      const float m = over_lanes<L, 0>(live ? lv : -INFINITY, most);
-      w = live ? expf(lv - m) : 0.f;
-      const float sum = over_lanes<L, 0>(w, add);
-      w = live ? w / sum : 0.f;
-    } else {
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) z += l[j] > -INFINITY ? expf(l[j] - top) : 0.f;
-      z = over_lanes<L, 0>(z, add);
-      w = live ? expf(lv - top) / z : 0.f;
-    }
-  } else if (a.renormalize) {
-    // s = e^min(l,0) / (1 + e^-|l|): the common factor e^M of the largest min(l, 0) is left out
-    // of all, so that scores which are all tiny keep their ratios
-    const float m = over_lanes<L, 0>(live ? fminf(lv, 0.f) : -INFINITY, most);
-    w = live ? expf(fminf(lv, 0.f) - m) / (1.f + expf(-fabsf(lv))) : 0.f;
+  if (live) lv = a.by_score ? a.logits[(size_t)t * a.ld + e] : (float)without_id(mine);
+  const float m = a.renormalize ? over_lanes<L, 0>(exponent_of(a, live, lv), most) : 0.f;
+  float w = weight_of(a, live, lv, m, row_sums<L, V>(a, l, top));
+  if (a.renormalize) {
     const float sum = over_lanes<L, 0>(w, add);
-    w = live ? w / sum : 0.f;
-  } else {
-    w = live ? expf(fminf(lv, 0.f)) / (1.f + expf(-fabsf(lv))) : 0.f;
+    w = live ? w * rcp32(sum) : 0.f;
   }
   if (t < a.T && tl < a.k) {
     a.topk_ids[(size_t)t * a.k + tl] = e;
     a.topk_w[(size_t)t * a.k + tl] = a.scale * w;
-  }
-  if (a.token_flags) {
-    const float any = over_lanes<L, 0>(bad ? 1.f : 0.f, most);
-    if (t < a.T && tl == 0) a.token_flags[t] = any != 0.f ? 1 : 0;
   }
 }
 
@@ -388,23 +504,20 @@ hipError_t launch_route_scored(RouteScoredArgs a, hipStream_t stream) {
   if (a.T <= 0) return hipSuccess;
   if (a.k < 1 || a.k > kMaxTopk || a.G < 1 || a.G > 64 || a.S < 1 || a.topk_groups < 1)
     return hipErrorInvalidValue;
-  a.Gp = 1;
-  while (a.Gp < a.G) a.Gp *= 2;
+  a.log_gp = 0;
+  while ((1 << a.log_gp) < a.G) ++a.log_gp;
+  const int Gp = 1 << a.log_gp;
   a.vec = a.S % 4 == 0 && a.ld % 4 == 0 && (((uintptr_t)a.logits | (uintptr_t)a.bias) & 15u) == 0
               ? 1
               : 0;
-  const int v16 = a.Gp <= 16 ? (a.S + 16 / a.Gp - 1) / (16 / a.Gp) : 1 << 20;
-  const int v64 = (a.S + 64 / a.Gp - 1) / (64 / a.Gp);
-  // 16 lanes a token once there are tokens enough to fill the chip
-  if (v16 <= 16 && a.T > 2048) {
-    if (a.vec && v16 <= 4) return launch_lv<16, 4>(a, stream);
-    if (v16 <= 1) return launch_lv<16, 1>(a, stream);
-    if (v16 <= 4) return launch_lv<16, 4>(a, stream);
-    if (v16 <= 8) return launch_lv<16, 8>(a, stream);
-    return launch_lv<16, 16>(a, stream);
-  }
-  if (v64 <= 1 && !a.vec) return launch_lv<64, 1>(a, stream);
-  if (v64 <= 4) return launch_lv<64, 4>(a, stream);
+  const int v16 = Gp <= 16 ? (a.S + 16 / Gp - 1) / (16 / Gp) : 1 << 20;
+  const int v64 = (a.S + 64 / Gp - 1) / (64 / Gp);
+  // 16 lanes a token wherever they hold it (a whole wavefront a token measured slower at every T: one
+  // token of 16 experts 3.3 against 3.0 us, 65536 of 256 85 against 35)
+  if (v16 <= 1 && !a.vec) return launch_lv<16, 1>(a, stream);
+  if (v16 <= 4) return launch_lv<16, 4>(a, stream);
+  if (v16 <= 8) return launch_lv<16, 8>(a, stream);
+  if (v16 <= 16) return launch_lv<16, 16>(a, stream);
   if (v64 <= 16) return launch_lv<64, 16>(a, stream);
   if (v64 <= 32) return launch_lv<64, 32>(a, stream);
   return hipErrorInvalidValue;

@@ -68,8 +68,8 @@ def _weight_bound(logits, k, w):
     """Relative error of a weight in units of 2^-23: an exponential and its sum's terms 4 each, the
     rounding of its argument (half a unit of it) twice, the sum over up to 38 partial sums, the
     division and the scaling; results under 2^-126 may be flushed."""
-    fin = np.where(np.isfinite(logits), logits, np.nan)
-    span = np.nan_to_num(np.nanmax(fin, 1) - np.nanmin(fin, 1), nan=0.0)
+    fin = np.isfinite(logits)
+    span = np.maximum(np.where(fin, logits, -np.inf).max(1) - np.where(fin, logits, np.inf).min(1), 0.0)
     return np.abs(w) * ((38 + 12 + np.minimum(span, 200.0))[:, None] * 2.0 ** -23) + 2.0 ** -125
 
 
@@ -172,6 +172,27 @@ def test_route_far_logits(spread, shift, scoring):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 2100])
+@pytest.mark.parametrize("E,k,G,tg", [(64, 8, 1, 1), (256, 8, 8, 4), (400, 16, 1, 1), (48, 5, 4, 1), (16, 2, 1, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_choices_closer_than_fp32(T, E, k, G, tg, scoring):
+    """Biases that bring every choice value of one token to within an fp32 rounding (6e-8) of 0.7:
+    neighbours, group sums and the last slot's border are told apart in double."""
+    L = _logits(1, E, 23)
+    l = L[0].double()
+    s = torch.softmax(l, 0) if scoring == "softmax" else torch.sigmoid(l)
+    bias = (0.7 - s).float()
+    c = (s + bias.double()).numpy()
+    gaps = np.diff(np.sort(c))
+    assert gaps.max() < 1e-7 and np.median(gaps) > 2e-12  # (told apart by 2^-42 = 2.3e-13)
+    rows = L.repeat(T, 1)
+    if T > 2:
+        rows[::2] = _logits((T + 1) // 2, E, 24)  # others beside it in the wavefront
+    _check(rows, k, bias, scoring=scoring, n_groups=G, topk_groups=tg, group_score="top2")
+    _check(rows, k, bias, scoring=scoring, n_groups=G, topk_groups=tg, group_score="max")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [17, 2100])
 def test_route_strided_and_unaligned_rows(T):
     wide = torch.randn(T, 77, device=DEV)
@@ -223,7 +244,7 @@ def _call(ptrs=None, **kw):
     dict(n_experts=4, topk=5), dict(scoring=2), dict(scoring=-1), dict(n_groups=0), dict(n_groups=3),
     dict(n_experts=130, n_groups=65, topk_groups=65, logits_stride=130), dict(topk_groups=0),
     dict(n_groups=4, topk_groups=5), dict(n_groups=16, topk_groups=1), dict(group_score=2), dict(renormalize=2),
-    dict(scale=math.inf), dict(scale=math.nan), dict(logits_stride=15)])
+    dict(scale=math.inf), dict(scale=math.nan), dict(logits_stride=15), dict(logits_stride=1 << 22)])
 def test_route_refuses_fields_out_of_range(bad):
     assert _call(**bad) == ml.EINVAL_DIMS
 
