@@ -179,9 +179,6 @@ int moe_lora_linear(const void* x, const void* W, const float* w_scale, const vo
   a.K = d->in_features;
   a.rows = (int64_t)d->out_features * (d->act == MOELORA_ACT_SWIGLU ? 2 : 1);
   a.act = d->act;
-  const uint64_t low = (uint64_t)(uintptr_t)y | (uint64_t)(uintptr_t)residual | (uint64_t)(2 * a.ldy) |
-                       (uint64_t)(2 * a.ldr);
-  a.vec = low % 16 == 0 ? 16 : (low % 8 == 0 ? 8 : 2);
   a.part = (float*)workspace;
   a.splits = 1;
   a.row_tiles = a.col_tiles = 0;

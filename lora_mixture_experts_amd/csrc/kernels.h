@@ -183,7 +183,6 @@ struct LinearArgs {
   int T, N, K;
   int64_t rows;  // weight rows: N, or 2 N for SwiGLU
   int act;
-  int vec;  // bytes of the largest access that rows of y and of the residual allow: 2, 8 or 16
   // tiled
   float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
   int splits, row_tiles, col_tiles;

@@ -111,6 +111,36 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
     ld.we[i] = (W8 ? 16 : 8) * c < rem ? ld.wo[i] : kOutOfRange;
   }
 
+  // The epilogue (below) finishes 32 rows at a time; a lane's share of them is ITS pieces of 8
+  // consecutive columns. Scales and biases are loaded before the main loop, and with one group of rows
+  // the residual too: their latency hides behind it.
+  const int fr = lane & 31, fg = lane >> 5;
+  constexpr int FO = GATED ? FN / 2 : FN, OC = FO * 32;        // output fragments and columns
+  constexpr int TP = 32 * OC / 512, ITS = (TP + KG - 1) / KG;  // pieces of a lane: all, one K group's
+  constexpr int REGION = 32 * WN;                              // floats
+  const bool split = a.splits > 1;
+  const int tc = col0 + wn * OC;
+  float sc[FN];
+  uint16_t bi[FN];  // (converted in the epilogue: here that would wait for the loads)
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int r = wn * WN + j * 32 + fr;
+    const int64_t row = col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0);
+    const bool in = !split && col0 + col_of(r) < a.N;
+    sc[j] = W8 && in ? a.wscale[row] : 1.f;
+    bi[j] = a.bias && in && kg == 0 ? a.bias[row] : (uint16_t)0;
+  }
+  auto first_of = [&](int it) { return ((it * KG + kg) * 64 + lane) * 8; };  // among the 32 x OC
+  Residual<8> res[ITS];
+  auto load_residual = [&](int i) {
+#pragma unroll
+    for (int it = 0; it < ITS; ++it)
+      if (it * KG + kg < TP)
+        res[it].load(a, row0 + wm * WM + i * 32 + first_of(it) / OC, tc + first_of(it) % OC);
+  };
+  const bool has_res = a.R && !split;
+  if (FM == 1 && has_res) load_residual(0);
+
   f32x16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -124,125 +154,79 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
   // at a time. A lane holds rows 8*(v/4) + 4*(lane/32) + v%4 of each 32-row group and column lane%32
   // of each fragment: each wavefront writes scale * sum (+ bias) row-major into its own region,
   // columns 32 apart swapped on every other run of 4 rows (the two halves of the wavefront hold rows 4
-  // apart: different banks). Then a lane reads 8 columns back, of all K groups, and finishes them:
-  // 8 consecutive ones where 16-byte accesses of y and the residual are possible, else columns 64
-  // apart, so that a store covers 128 consecutive bytes. The residual's loads go out before the values
-  // are written.
-  const int fr = lane & 31, fg = lane >> 5;
-  constexpr int FO = GATED ? FN / 2 : FN, OC = FO * 32;  // output fragments and columns
-  constexpr int TP = 32 * OC / 512, ITS = (TP + KG - 1) / KG;  // pieces of 8 columns per lane: all, a group's
-  constexpr int REGION = 32 * WN;                        // floats
+  // apart: different banks). Then the lanes read their pieces back, of all K groups, and finish them.
   float* const all = reinterpret_cast<float*>(lds);
   float* const own = all + wave_all * REGION;
-  const bool split = a.splits > 1, wide = a.vec >= 16;
-  float sc[FN], bi[FN];
-#pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int r = wn * WN + j * 32 + fr;
-    const int64_t row = col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0);
-    ScaleBias<1> sb;
-    sb.load(a, row, !split && col0 + col_of(r) < a.N ? row + 1 : row);
-    sc[j] = sb.s[0];
-    bi[j] = kg == 0 ? sb.b[0] : 0.f;
-  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int tr = row0 + wm * WM + i * 32, tc = col0 + wn * OC;
-    Residual<8> res[ITS];
-    if (!split && wide) {
-#pragma unroll
-      for (int it = 0; it < ITS; ++it) {
-        if (it * KG + kg >= TP) continue;
-        const int f = ((it * KG + kg) * 64 + lane) * 8;
-        res[it].load(a, tr + f / OC, tc + f % OC);
-      }
-    }
+    const int tr = row0 + wm * WM + i * 32;
+    if (FM > 1 && has_res) load_residual(i);
     if (KG > 1 && i > 0) __syncthreads();  // the other groups have read the rows before
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int r = 8 * (v / 4) + 4 * fg + v % 4;
 #pragma unroll
-      for (int j = 0; j < FN; ++j) own[r * WN + ((j * 32 + fr) ^ (32 * fg))] = acc[i][j][v] * sc[j] + bi[j];
+      for (int j = 0; j < FN; ++j) own[r * WN + ((j * 32 + fr) ^ (32 * fg))] = acc[i][j][v] * sc[j] + bf16_to_f32(bi[j]);
     }
     if (KG > 1) __syncthreads();
     else __builtin_amdgcn_wave_barrier();
     // column c of row r, all K groups (WN/2 further: the up half)
+    auto at = [&](int r, int c) { return all + wave * REGION + r * WN + (c ^ (32 * ((r >> 2) & 1))); };
     auto sum4 = [&](int r, int c) {
-      const float* p = all + wave * REGION + r * WN + (c ^ (32 * ((r >> 2) & 1)));
+      const float* p = at(r, c);
       f32x4 s = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
       for (int g = 1; g < KG; ++g) s += *reinterpret_cast<const f32x4*>(p + g * NWV * REGION);
       return s;
     };
-    auto sum1 = [&](int r, int c) {
-      const float* p = all + wave * REGION + r * WN + (c ^ (32 * ((r >> 2) & 1)));
-      float s = *p;
-#pragma unroll
-      for (int g = 1; g < KG; ++g) s += p[g * NWV * REGION];
-      return s;
-    };
     if (split) {
       float* part = a.part + (int64_t)sp * a.T * a.rows;
 #pragma unroll 4
-      for (int f0 = kg * 64; f0 < 32 * WN; f0 += KG * 64) {
-        const int r = (f0 + lane) / WN, c = (f0 + lane) % WN;
+      for (int f = (kg * 64 + lane) * 4; f < 32 * WN; f += KG * 256) {
+        const int r = f / WN, c = f % WN;
         const int n = tc + (GATED ? c % (WN / 2) : c);
-        if (tr + r < a.T && n < a.N)
-          part[(int64_t)(tr + r) * a.rows + n + (GATED && c >= WN / 2 ? (int64_t)a.N : 0)] = sum1(r, c);
-      }
-    } else if (wide) {
-      if (!GATED && KG == 1 && a.act != kActNone) {
-        // (a loop that is not unrolled: unrolled over the accumulators, activations spilled them)
-#pragma unroll 1
-        for (int it = 0; it < ITS; ++it) {
-          float* p = own + (it * 64 + lane) * 8;  // (any share of the values will do)
-          float o[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = p[e];
-          linear_act(a.act, o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = o[e];
+        if (tr + r >= a.T || n >= a.N) continue;
+        float* to = part + (int64_t)(tr + r) * a.rows + n + (GATED && c >= WN / 2 ? (int64_t)a.N : 0);
+        const f32x4 v = sum4(r, c);
+        if (n + 4 <= a.N) {
+          *reinterpret_cast<f32x4_any*>(to) = v;
+        } else {
+          for (int e = 0; n + e < a.N; ++e) to[e] = v[e];
         }
-        __builtin_amdgcn_wave_barrier();
       }
-#pragma unroll
+      continue;
+    }
+    if (!GATED && KG == 1 && a.act != kActNone) {
+      // in place, in a loop that is not unrolled: unrolled over the accumulators, activations spilled
+      // them
+#pragma unroll 1
       for (int it = 0; it < ITS; ++it) {
-        if (it * KG + kg >= TP) continue;
-        const int f = ((it * KG + kg) * 64 + lane) * 8, r = f / OC, c = f % OC;
+        float* p = own + (it * 64 + lane) * 8;  // (any share of the values will do)
         float o[8];
 #pragma unroll
-        for (int q = 0; q < 8; q += 4) {
-          const f32x4 g = sum4(r, c + q);
-          f32x4 u = {0.f, 0.f, 0.f, 0.f};
-          if (GATED) u = sum4(r, c + q + WN / 2);
+        for (int e = 0; e < 8; ++e) o[e] = p[e];
+        linear_act(a.act, o);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[q + e] = GATED ? swiglu(g[e], u[e]) : g[e];
-        }
-        if (!GATED && KG > 1) linear_act(a.act, o);
-        linear_store(a, tr + r, tc + c, o, res[it]);
+        for (int e = 0; e < 8; ++e) p[e] = o[e];
       }
-    } else {
-#pragma unroll 1
-      for (int it = 0; it < ITS; ++it) {
-        if (it * KG + kg >= TP) break;
-        const int f = (it * KG + kg) * 512 + lane;
-        float o[8], add[8];
+      __builtin_amdgcn_wave_barrier();
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = (f + 64 * e) / OC, c = (f + 64 * e) % OC, t = tr + r, n = tc + c;
-          add[e] = a.R && t < a.T && n < a.N ? bf16_to_f32(a.R[(int64_t)t * a.ldr + n]) : 0.f;
-          const float g = sum1(r, c);
-          o[e] = GATED ? swiglu(g, sum1(r, c + WN / 2)) : g;
-        }
-        if (!GATED) linear_act(a.act, o);
+    for (int it = 0; it < ITS; ++it) {
+      if (it * KG + kg >= TP) continue;
+      const int r = first_of(it) / OC, c = first_of(it) % OC;
+      float o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = (f + 64 * e) / OC, c = (f + 64 * e) % OC, t = tr + r, n = tc + c;
-          if (t < a.T && n < a.N)
-            a.Y[(int64_t)t * a.ldy + n] = (uint16_t)f32_to_bf16_bits(a.R ? o[e] + add[e] : o[e]);
-        }
+      for (int q = 0; q < 8; q += 4) {
+        const f32x4 g = sum4(r, c + q);
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
+        if (GATED) u = sum4(r, c + q + WN / 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[q + e] = GATED ? swiglu(g[e], u[e]) : g[e];
       }
+      if (!GATED && KG > 1) linear_act(a.act, o);
+      linear_store(a, tr + r, tc + c, o, res[it]);
     }
     if (KG == 1) __builtin_amdgcn_wave_barrier();
   }
@@ -265,10 +249,10 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearArgs a) {
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
     const float* src = a.part + (int64_t)t * a.rows + (int64_t)h * a.N + n;
-    if (a.rows % 4 == 0 && a.N % 4 == 0) {
+    if (n + 4 <= a.N) {
 #pragma unroll
       for (int s = 0; s < kMaxLinearSplits; ++s)
-        p[h][s] = *reinterpret_cast<const f32x4*>(src + min(s, a.splits - 1) * stride);
+        p[h][s] = *reinterpret_cast<const f32x4_any*>(src + min(s, a.splits - 1) * stride);
     } else {
 #pragma unroll
       for (int s = 0; s < kMaxLinearSplits; ++s)
