@@ -7,6 +7,15 @@
 
 namespace moelora {
 
+// The hardware's reciprocal (a unit in the last place, far below the outputs' rounding; a division is
+// ten instructions) and its conversion of two floats to bf16, to nearest even.
+__device__ __forceinline__ float one_over(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Activation of C values (SwiGLU takes two of them: swiglu below). The exponentials of large
 // arguments run into infinity or zero, which gives the activations' limits.
 template <int C>
@@ -18,7 +27,7 @@ __device__ __forceinline__ void linear_act(int act, float (&v)[C]) {
       break;
     case kActSilu:
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] = v[c] / (1.f + __expf(-v[c]));
+      for (int c = 0; c < C; ++c) v[c] *= one_over(1.f + __expf(-v[c]));
       break;
     case kActGelu:  // x * Phi(x) with Phi(x) = erfc(-x / sqrt 2) / 2: no cancellation for negative x
 #pragma unroll
@@ -27,13 +36,13 @@ __device__ __forceinline__ void linear_act(int act, float (&v)[C]) {
     case kActGeluTanh:  // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        v[c] = v[c] / (1.f + __expf(-1.5957691f * v[c] * (1.f + 0.044715f * v[c] * v[c])));
+        v[c] *= one_over(1.f + __expf(-1.5957691f * v[c] * (1.f + 0.044715f * v[c] * v[c])));
       break;
     default:
       break;
   }
 }
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+__device__ __forceinline__ float swiglu(float g, float u) { return g * one_over(1.f + __expf(-g)) * u; }
 
 // Accesses of 8 or 16 bytes at any element of a row: the hardware takes them at 2-byte alignment
 // (rows of y and of the residual may have any stride), and one that crosses a line costs one more
@@ -87,13 +96,13 @@ __device__ __forceinline__ void linear_store(const LinearArgs& a, int t, int n, 
   if (n + C <= a.N) {
     uint32_t w[C / 2];
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < C / 2; ++i) w[i] = to_bf16x2(v[2 * i], v[2 * i + 1]);
     if constexpr (C == 8) *reinterpret_cast<u32x4_any*>(y) = u32x4{w[0], w[1], w[2], w[3]};
     else *reinterpret_cast<u32x2_any*>(y) = u32x2{w[0], w[1]};
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      if (n + i < a.N) y[i] = (uint16_t)f32_to_bf16_bits(v[i]);
+      if (n + i < a.N) y[i] = (uint16_t)to_bf16x2(v[i], 0.f);
   }
 }
 

@@ -25,11 +25,11 @@ namespace {
 constexpr int kStreamWaves = 8;
 }
 
-// NT: 16-row token tiles.
+// NT: 16-row token tiles. STREAM: the weights with the non-temporal hint.
 // A load at or past the end of its row (K is a multiple of 8, not of 64) or of a row past the end
 // gets an out-of-range offset: zeros, no traffic. Every load is unconditional, also in the last
 // steps, so the count of loads in flight that the compiler waits for stays exact.
-template <int NT, bool GATED, bool W8>
+template <int NT, bool GATED, bool W8, bool STREAM = false>
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
   constexpr int WK = kStreamWaves;
   constexpr int NH = GATED ? 2 : 1;  // weight rows of an output: gate and up
@@ -82,7 +82,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 #pragma unroll
       for (int j = 0; j < WL; ++j) {
         const int kk = k + KJ * j;
-        s.w[h][j] = bufld16(wr[h], kk < K ? wo + (uint32_t)(kk * WB) : kOutOfRange);
+        const uint32_t off = kk < K ? wo + (uint32_t)(kk * WB) : kOutOfRange;
+        s.w[h][j] = STREAM ? bufld16_nt(wr[h], off) : bufld16(wr[h], off);
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -150,6 +151,9 @@ hipError_t launch_nt(const LinearArgs& a, hipStream_t stream) {
   if (a.wscale) {
     if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, true>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((linear_stream_kernel<NT, false, true>), grid, block, 0, stream, a);
+  } else if (a.stream_w) {
+    if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, false, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((linear_stream_kernel<NT, false, false, true>), grid, block, 0, stream, a);
   } else {
     if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, false>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((linear_stream_kernel<NT, false, false>), grid, block, 0, stream, a);

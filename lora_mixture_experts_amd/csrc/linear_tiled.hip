@@ -24,7 +24,8 @@ namespace moelora {
 
 // Loads of a tile: rows past the end have out-of-range offsets (zeros); the last step of a K that
 // is not a multiple of the step's width is loaded with the chunks past the end out of range.
-template <class Pipe, bool W8>
+// STREAM: the weights with the non-temporal hint (one row tile: nobody else reads them).
+template <class Pipe, bool W8, bool STREAM>
 struct LinearLoader {
   static constexpr int NA = Pipe::NA, NB = Pipe::NB, BKS = Pipe::SUB * 16;
   u32x4 xr, wr[NB];         // (a block of weight rows is all gate rows or all up rows)
@@ -35,6 +36,7 @@ struct LinearLoader {
   __device__ __forceinline__ void prep(int) {}
   __device__ __forceinline__ void load_main(int d, int ks, uint32_t lds_addr) {
     if (d < NA) lds_dma16(xr, xo[d], (uint32_t)ks * BKS * 2, lds_addr);
+    else if (STREAM) lds_dma16_nt(wr[d - NA], wo[d - NA], (uint32_t)ks * Pipe::BROW, lds_addr);
     else lds_dma16(wr[d - NA], wo[d - NA], (uint32_t)ks * Pipe::BROW, lds_addr);
   }
   __device__ __forceinline__ void load(int d, int ks, uint32_t lds_addr) {
@@ -48,7 +50,7 @@ struct LinearLoader {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8>
+template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8, bool STREAM = false>
 __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_tiled_kernel(LinearArgs a) {
   constexpr int NWV = (BM / WM) * (BN / WN);
   using Pipe = TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>;
@@ -91,7 +93,7 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
   auto col_of = [&](int r) { return GATED ? (r / WN) * (WN / 2) + r % (WN / 2) : r; };
   auto is_up = [&](int r) { return GATED && r % WN >= WN / 2; };
 
-  LinearLoader<Pipe, W8> ld;
+  LinearLoader<Pipe, W8, STREAM> ld;
   ld.full = klen / 64;
   const int rem = klen - ld.full * 64;
   ld.xr = buffer_desc(a.X + (int64_t)row0 * a.ldx + k0, 0x7fffffffu);
@@ -279,14 +281,14 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearArgs a) {
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8>
+template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8, bool STREAM = false>
 hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
   constexpr int NWV = (BM / WM) * (BN / WN);
   constexpr int ring = KG * TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>::LDS_BYTES;
   constexpr int out = KG * NWV * 32 * WN * 4;  // the epilogue's regions
   constexpr int bytes = ring > out ? ring : out;
   static_assert(bytes <= kLdsBytes, "LDS stages must fit");
-  auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, KG, GATED, W8>;
+  auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, KG, GATED, W8, STREAM>;
   static bool attr_set[64] = {};
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -317,6 +319,9 @@ hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t st
   const int on = gated ? p.bn / 2 : p.bn;
   a.col_tiles = (a.N + on - 1) / on;
   if (a.splits < 1 || a.splits > kMaxLinearSplits || (a.splits > 1 && !a.part)) return hipErrorInvalidValue;
+  if (a.stream_w && p.bm == 64 && p.bn == 128)
+    return gated ? launch_tile<64, 128, 32, 64, 3, 2, true, false, true>(a, stream)
+                 : launch_tile<64, 128, 32, 64, 3, 2, false, false, true>(a, stream);
 #define MOELORA_LINEAR(BM_, BN_, WM_, WN_, NST_, KG_)                                           \
   if (p.bm == BM_ && p.bn == BN_ && p.nst == NST_ && p.kg == KG_) {                              \
     if (w8)                                                                                      \

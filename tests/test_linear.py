@@ -223,7 +223,7 @@ def test_linear_graph_replays(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [12, 96])
+@pytest.mark.parametrize("T", [12, 40, 96])
 def test_linear_weights_past_4_gib(T):
     """Weight rows whose byte offsets pass 32 bits: the last rows of a 5 GiB matrix (4 GiB between
     gate and up)."""
