@@ -775,16 +775,14 @@ int moe_lora_forward_topk(const void* x, const int32_t* topk_ids, const float* t
                           void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_given_dims(d, topk);
   if (rc != MOELORA_OK) return rc;
+  if (d->T > 0 && !topk_ids) return MOELORA_ENULL;
+  if (d->T > 0 && !aligned16(topk_ids)) return MOELORA_EALIGN;
   const bool fp8 = W1_scale || W2_scale;
   ForwardPlan pl;
   MoeLoraLayout L;
   // (topk_w takes the place of the logits in the checks)
   rc = check_forward(x, topk_w, nullptr, W1, W2, A1, B1, A2, B2, adapter_ids, topk, d, y, workspace,
                      workspace_bytes, W1_scale, W2_scale, fp8, &pl, &L);
-  if (rc == MOELORA_OK || rc == MOELORA_EHIP || rc == MOELORA_EDEVICE) {
-    if (d->T > 0 && !topk_ids) return MOELORA_ENULL;
-    if (d->T > 0 && !aligned16(topk_ids)) return MOELORA_EALIGN;
-  }
   if (rc != MOELORA_OK || d->T == 0) return rc;
   return enqueue_forward(pl, L, x, nullptr, nullptr, W1, W2, A1, B1, A2, B2, adapter_ids, topk, d, y,
                          (char*)workspace, (hipStream_t)stream, nullptr, W1_scale, W2_scale, topk_ids,

@@ -54,7 +54,7 @@ int validate_linear(const moe_lora_linear_dims* d, bool residual) {
 // types, with and without SwiGLU) on which every kernel, tile and split was timed. Its choice is on
 // average 2% and in nine shapes of ten at most 8% above the fastest; without the streaming kernel
 // the fastest left is 10% slower on average, without the 64 x 64, 64 x 128, 128 x 128 or 256 x 256
-// tile 1.5%, 1%, 2.3% or 1%.
+// tile 1.5%, 1%, 2.3% or 1%. bm = 0 without `stream`: more tiles than a launch can hold.
 LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   const bool gated = d->act == MOELORA_ACT_SWIGLU, w8 = d->w_type == MOELORA_W_E4M3;
   const double rows = (double)d->out_features * (gated ? 2 : 1), wb = w8 ? 1.0 : 2.0;
@@ -84,6 +84,7 @@ LinearPlan plan_linear(const moe_lora_linear_dims* d) {
     const double n = ((d->T + t.bm - 1) / t.bm) * std::ceil(rows / t.bn);
     for (int s = 1; s <= kMaxLinearSplits; ++s) {
       if (s > 1 && (steps / s < 4 || n * s > 600)) break;
+      if (n * s >= (1 << 23) - 64) break;  // 512 threads each: what a launch can hold
       const int chain = (steps + s * t.kg - 1) / (s * t.kg);
       // a round lasts for its steps, or for the weight bytes of the workgroups it runs
       const double round = std::max(t.round + chain * (w8 ? t.step8 : t.step),
@@ -158,6 +159,7 @@ int moe_lora_linear(const void* x, const void* W, const float* w_scale, const vo
   if (!aligned16(x) || !aligned16(W) || ((uintptr_t)w_scale & 3u) != 0) return MOELORA_EALIGN;
   if ((((uintptr_t)bias | (uintptr_t)residual | (uintptr_t)y) & 1u) != 0) return MOELORA_EALIGN;
   const LinearPlan p = plan_linear(d);
+  if (!p.stream && p.bm == 0) return MOELORA_EINVAL_DIMS;
   const size_t need = linear_workspace(d, p);
   if (need && !workspace) return MOELORA_ENULL;
   if (need && (((uintptr_t)workspace & 255u) != 0 || workspace_bytes < need)) return MOELORA_EWORKSPACE;

@@ -299,7 +299,6 @@ hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
     attr_set[dev] = true;
   }
   const int64_t live = (int64_t)a.row_tiles * a.col_tiles * a.splits;
-  if (live * 64 * NWV * KG >= ((int64_t)1 << 32) - 4096) return hipErrorInvalidValue;  // threads of a launch
   const unsigned grid = (unsigned)((live + 7) / 8 * 8);
   hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * NWV * KG), bytes, stream, a);
   err = hipGetLastError();

@@ -286,6 +286,11 @@ def test_linear_refuses_pointers():
     assert _call(T=0, ptrs={k: None for k in PTRS}) == ml.OK
 
 
+def test_linear_refuses_more_tiles_than_a_launch_holds():
+    big = dict(T=(1 << 30) - 1, out_features=1 << 20, y_stride=1 << 20, residual_stride=1 << 20)
+    assert _call(**big) == ml.EINVAL_DIMS
+
+
 def test_linear_refuses_workspaces():
     big = dict(T=100, in_features=8192, x_stride=8192, w_stride=8192)
     d = ml.LinearDims(**{**FIELDS, **big})
