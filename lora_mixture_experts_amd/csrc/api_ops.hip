@@ -50,11 +50,12 @@ int validate_linear(const moe_lora_linear_dims* d, bool residual) {
 }
 
 // Kernel, tile and reduction splits of a call, from its sizes alone: the least of an estimate in
-// microseconds, fitted to 3 700 shapes (T 1 to 4096, K 128 to 14 000, N 64 to 14 000, both weight
+// microseconds, fitted to 7 100 shapes (T 1 to 6000, K 128 to 14 000, N 64 to 14 000, both weight
 // types, with and without SwiGLU) on which every kernel, tile and split was timed. Its choice is on
-// average 2% and in nine shapes of ten at most 8% above the fastest; without the streaming kernel
-// the fastest left is 10% slower on average, without the 64 x 64, 64 x 128, 128 x 128 or 256 x 256
-// tile 1.5%, 1%, 2.3% or 1%. bm = 0 without `stream`: more tiles than a launch can hold.
+// average 1% above the fastest, in nine shapes of ten at most 2%, in 99 of 100 at most 18%; without
+// the streaming kernel the choice is 8% above on average (18% up to 64 tokens), without the 64 x 64,
+// 64 x 128, 128 x 128 or 256 x 256 tile 6%, 3%, 4% or 2.5%. bm = 0 without `stream`: more tiles than
+// a launch can hold.
 LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   const bool gated = d->act == MOELORA_ACT_SWIGLU, w8 = d->w_type == MOELORA_W_E4M3;
   const double rows = (double)d->out_features * (gated ? 2 : 1), wb = w8 ? 1.0 : 2.0;
@@ -67,19 +68,19 @@ LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   // past that the token rows outweigh the weights.
   const int groups = (d->out_features + 15) / 16;
   if (d->T <= 32 || (d->T <= kLinearStreamTokens && groups <= 256)) {
-    const double step = d->T <= 16 ? 0.53 : (d->T <= 32 ? 1.05 : 1.7);
-    const double chain = step * ((steps + 7) / 8) * (gated ? 1.4 : 1.0) * (w8 ? 0.78 : 1.0) *
+    const double step = d->T <= 16 ? 0.57 : (d->T <= 32 ? 1.2 : 1.4);
+    const double chain = step * ((steps + 7) / 8) * (gated ? 1.4 : 1.0) * (w8 ? 0.8 : 1.0) *
                          std::max(1.0, groups / 256.0);
-    least = 4.8 + std::max(chain, rows * d->in_features * wb / 5.0e6);
+    least = 5.2 + std::max(chain, rows * d->in_features * wb / 5.6e6);
     best.stream = true;
   }
   static const struct {
     int bm, bn, nst, kg;
     double fixed, round, step, step8;  // a call, a round of 256 workgroups, a step of all K groups
-  } tiles[] = {{64, 64, 2, 4, 1.7, 4.4, 1.0, 1.08},
-               {64, 128, 3, 2, 2.5, 4.7, 0.56, 0.67},
-               {128, 128, 3, 1, 8.0, 0.0, 0.40, 0.47},
-               {256, 256, 2, 1, 3.0, 9.3, 0.97, 1.2}};
+  } tiles[] = {{64, 64, 2, 4, 1.5, 4.4, 0.96, 0.97},
+               {64, 128, 3, 2, 2.1, 4.4, 0.63, 0.65},
+               {128, 128, 3, 1, 5.1, 2.3, 0.43, 0.47},
+               {256, 256, 2, 1, 3.0, 8.8, 0.99, 1.5}};
   for (const auto& t : tiles) {
     const double n = ((d->T + t.bm - 1) / t.bm) * std::ceil(rows / t.bn);
     for (int s = 1; s <= kMaxLinearSplits; ++s) {
@@ -88,9 +89,9 @@ LinearPlan plan_linear(const moe_lora_linear_dims* d) {
       const int chain = (steps + s * t.kg - 1) / (s * t.kg);
       // a round lasts for its steps, or for the weight bytes of the workgroups it runs
       const double round = std::max(t.round + chain * (w8 ? t.step8 : t.step),
-                                    std::min(n * s, 256.0) * t.bn * 64 * wb * steps / s / 8.5e6);
+                                    std::min(n * s, 256.0) * t.bn * 64 * wb * steps / s / 1.0e7);
       double us = t.fixed + std::ceil(n * s / 256) * round;
-      if (s > 1) us += 3.8 + 2.1e-6 * s * d->T * rows;  // the second launch and the sums it reads
+      if (s > 1) us += 4.0 + 1.4e-6 * s * d->T * rows;  // the second launch and the sums it reads
       if (us < least) {
         least = us;
         best = LinearPlan{false, t.bm, t.bn, t.nst, t.kg, s};

@@ -74,11 +74,6 @@ __device__ __forceinline__ u32x4 bufld16(__amdgpu_buffer_rsrc_t r, uint32_t byte
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte_off, 0, 0);
 }
 
-// As bufld16 with the non-temporal hint: for bytes that are read once.
-__device__ __forceinline__ u32x4 bufld16_nt(__amdgpu_buffer_rsrc_t r, uint32_t byte_off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte_off, 0, 2);
-}
-
 __device__ __forceinline__ uint64_t lanemask_lt() {
   return (1ull << (threadIdx.x & 63)) - 1ull;
 }

@@ -183,7 +183,7 @@ struct LinearArgs {
   int T, N, K;
   int64_t rows;  // weight rows: N, or 2 N for SwiGLU
   int act;
-  int stream_w;  // weights with the non-temporal hint (64-row tiles and the streaming kernel)
+  int stream_w;  // weights with the non-temporal hint (64 x 128 tiles)
   // tiled
   float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
   int splits, row_tiles, col_tiles;

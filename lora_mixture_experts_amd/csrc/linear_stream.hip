@@ -13,8 +13,9 @@
 // (three or four sets, two chunks a step and 32 columns a workgroup measured 2 to 40% slower). What
 // the epilogue adds is loaded first, so that it costs no round trip at the end.
 //
-// Measured: one token, 4096 x 4096 bf16 8.5 us (4.0 TB/s), 22016 x 4096 35 us (5.1 TB/s: the rate
-// of a large copy); 16 tokens 10.4 us and 40.5 us.
+// Measured: 4096 x 4096 bf16, one token 8.3 us (4.0 TB/s), 16 tokens 10.2. From some 80 MB of
+// weights on the tiled kernel, whose workgroups read longer pieces of more rows, is the faster
+// one (one token, 8541 x 8768: 31 us against 45).
 #include "common.h"
 #include "kernels.h"
 #include "linear.h"
@@ -25,11 +26,11 @@ namespace {
 constexpr int kStreamWaves = 8;
 }
 
-// NT: 16-row token tiles. STREAM: the weights with the non-temporal hint.
+// NT: 16-row token tiles.
 // A load at or past the end of its row (K is a multiple of 8, not of 64) or of a row past the end
 // gets an out-of-range offset: zeros, no traffic. Every load is unconditional, also in the last
 // steps, so the count of loads in flight that the compiler waits for stays exact.
-template <int NT, bool GATED, bool W8, bool STREAM = false>
+template <int NT, bool GATED, bool W8>
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
   constexpr int WK = kStreamWaves;
   constexpr int NH = GATED ? 2 : 1;  // weight rows of an output: gate and up
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
       for (int j = 0; j < WL; ++j) {
         const int kk = k + KJ * j;
         const uint32_t off = kk < K ? wo + (uint32_t)(kk * WB) : kOutOfRange;
-        s.w[h][j] = STREAM ? bufld16_nt(wr[h], off) : bufld16(wr[h], off);
+        s.w[h][j] = bufld16(wr[h], off);
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -151,9 +152,6 @@ hipError_t launch_nt(const LinearArgs& a, hipStream_t stream) {
   if (a.wscale) {
     if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, true>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((linear_stream_kernel<NT, false, true>), grid, block, 0, stream, a);
-  } else if (a.stream_w) {
-    if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, false, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((linear_stream_kernel<NT, false, false, true>), grid, block, 0, stream, a);
   } else {
     if (gated) hipLaunchKernelGGL((linear_stream_kernel<NT, true, false>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((linear_stream_kernel<NT, false, false>), grid, block, 0, stream, a);
