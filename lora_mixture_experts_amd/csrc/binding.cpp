@@ -131,7 +131,8 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
     r.scale = (float)scale;
     r.logits_stride = row_stride(logits, "logits");
-    const int64_t k = r.topk > 0 ? r.topk : 0;
+    // (a topk that moe_lora_route refuses allocates nothing first)
+    const int64_t k = r.topk > 0 && r.topk <= E ? r.topk : 0;
     Tensor ids, w;
     if (a[10] == Py_None) ids = at::empty({T, k}, logits.options().dtype(at::kInt));
     else ids = *tensor_of(a[10], "topk_ids");
@@ -155,6 +156,14 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(std::move(w)));
     return out;
   });
+}
+
+// Whether two tensors are sure to share bytes: the same start, or ranges of dense ones that meet
+// (column slices of one buffer interleave without sharing any).
+bool overlap(const Tensor& a, const Tensor& b) {
+  if (!a.numel() || !b.numel()) return false;
+  const char *p = (const char*)a.data_ptr(), *q = (const char*)b.data_ptr();
+  return p == q || (a.is_contiguous() && b.is_contiguous() && p < q + b.nbytes() && q < p + a.nbytes());
 }
 
 // linear(x, W, w_scale, bias, act, residual, y, workspace) -> y
@@ -198,6 +207,11 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(y, "y", at::kBFloat16, {T, N}, dev);
     }
     d.y_stride = row_stride(y, "y");
+    if (a[6] != Py_None) {
+      const bool in_place = residual == y.data_ptr() && (T == 1 || d.residual_stride == d.y_stride);
+      if (overlap(y, x) || overlap(y, W) || (residual && !in_place && overlap(y, *tensor_of(a[5], "residual"))))
+        refuse(PyExc_ValueError, "%s overlaps an input%s", "y");
+    }
     Tensor ws;
     if (a[7] != Py_None) {
       ws = *tensor_of(a[7], "workspace");

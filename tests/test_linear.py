@@ -309,3 +309,22 @@ def test_linear_binding_refuses():
         ml.linear(x, W, act="tanh")
     with pytest.raises(ValueError):
         ml.linear(x[0], W)
+
+
+@pytest.mark.gpu
+def test_linear_refuses_outputs_over_inputs():
+    """An output that shares bytes with x, W or a residual it is not in place of is refused; column
+    slices of one buffer share none."""
+    buf = torch.randn(8, 256, device=DEV).to(BF)
+    W = torch.randn(64, 64, device=DEV).to(BF)
+    x, y = buf[:, :64], buf[:, 64:128]
+    want = ml.linear(x, W)
+    flat = torch.empty(64 * 64 * 2, dtype=BF, device=DEV)
+    over = [(x, W, None, x), (x, W, flat[:512].view(8, 64), flat[64:576].view(8, 64)),
+            (x, W, buf[:, 64:128], buf.view(-1)[64:576].view(8, 64)), (x, flat[:4096].view(64, 64), None, flat[4032:4544].view(8, 64))]
+    for a, w, residual, out in over:
+        with pytest.raises(ValueError):
+            ml.linear(a, w, residual=residual, y=out)
+    assert torch.equal(ml.linear(x, W, y=y), want)
+    one = buf[:1, :64].clone()
+    assert torch.equal(ml.linear(x[:1], W, residual=one, y=one), one)

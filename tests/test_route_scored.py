@@ -270,3 +270,11 @@ def test_route_binding_refuses():
         ml.route(torch.zeros(4, 8, dtype=torch.float16), 2)
     with pytest.raises(ValueError):
         ml.route(torch.zeros(8), 2)
+
+
+@pytest.mark.gpu
+def test_route_refuses_choices_before_it_allocates():
+    logits = torch.randn(4, 32, device=DEV)
+    for k in (33, 2 ** 31 - 1, 0, -1):
+        with pytest.raises(ml.MoeLoraError):
+            ml.route(logits, k)
