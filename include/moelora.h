@@ -273,7 +273,9 @@ int moe_lora_workspace_layout(const moe_lora_dims *d, int32_t topk, moe_lora_lay
  *            with fewer experts to choose has expert -1 and weight 0 in the slots left;
  *   weight   scale * s_e, or with renormalize scale * s_e / (sum of the chosen s). The bias steers
  *            the choice and is no part of the weight.
- * Choice values are computed in double precision and told apart at 2^-42 of their size. */
+ * Choice values are computed in double precision and told apart at 2^-42 of their size. In them a
+ * sigmoid below e^-700 counts as e^-700, and an exponential of a softmax below 2^-1000 of the
+ * largest as 2^-1000 of it. */
 #define MOELORA_SCORE_SOFTMAX 0
 #define MOELORA_SCORE_SIGMOID 1
 #define MOELORA_GROUP_MAX 0

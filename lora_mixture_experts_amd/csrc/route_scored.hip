@@ -297,8 +297,10 @@ __device__ __forceinline__ void lane_list(const RouteScoredArgs& a, const LaneEx
         c32[j] = __builtin_fmaf(l[j], 0.f, s + x.b[j]);
         c = (double)c32[j];
       } else {
-        const double v = max64((double)l[j], -700.0);
-        const double s = SOFTMAX ? exp64(v - (double)top) * inv : rcp64(1.0 + exp64(-v));
+        // (softmax: only the distance to the largest matters, wherever the logits lie; sigmoid: e^700 is
+        // near the largest double)
+        const double v = (double)l[j];
+        const double s = SOFTMAX ? exp64(max64(v - (double)top, -1000.0)) * inv : rcp64(1.0 + exp64(-max64(v, -700.0)));
         c = s + (double)__builtin_fmaf(l[j], 0.f, x.b[j]);
       }
       key[j] = with_id<10>(max64(c, kNone), x.id(j));

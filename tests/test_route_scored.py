@@ -192,6 +192,31 @@ def test_route_choices_closer_than_fp32(T, E, k, G, tg, scoring):
     _check(rows, k, bias, scoring=scoring, n_groups=G, topk_groups=tg, group_score="max")
 
 
+def _far_rows(T, E, shift):
+    """By row, one of each to a wavefront of four: few levels around 0 (ties, which are settled in
+    double), normal logits moved by `shift`, one level there, every third expert switched off there."""
+    L = _logits(T, E, 29)
+    L[::4] = torch.round(L[::4])
+    L[1::4] += shift
+    L[2::4] = shift
+    L[3::4] += shift
+    L[3::4, ::3] = -math.inf
+    return L
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [-650.0, -700.0, -1000.0, -1500.0, -1e4, -1e9, 1e4])
+@pytest.mark.parametrize("E,k,G,tg", [(32, 4, 8, 4), (256, 8, 8, 3), (96, 5, 1, 1)])
+def test_route_far_logits_ranked_by_softmax_scores(shift, E, k, G, tg):
+    """A softmax depends on the differences of the logits only, wherever they lie."""
+    L = _far_rows(65, E, shift)
+    bias = 0.02 * _logits(1, E, 31)[0]
+    for b in (None, bias, torch.zeros(E)):
+        for group_score in ("top2", "max"):
+            _check(L, k, b, n_groups=G, topk_groups=tg, group_score=group_score, renormalize=False)
+            _check(L, k, b, n_groups=G, topk_groups=tg, group_score=group_score)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [17, 2100])
 def test_route_strided_and_unaligned_rows(T):
