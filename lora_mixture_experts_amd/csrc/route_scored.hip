@@ -30,7 +30,7 @@ namespace {
 
 constexpr double kNone = -1e300;  // value of an expert that cannot be chosen
 constexpr double kLeast = -1e299;  // keys above it can be
-constexpr float kBig = 3.4e38f;
+constexpr float kBig = 3.40282347e38f;  // the largest float: a finite logit may be its negative
 
 __device__ __forceinline__ double max64(double a, double b) {
   double r;  // (keys are never NaN: no canonicalising copies)

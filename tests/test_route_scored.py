@@ -218,6 +218,38 @@ def test_route_far_logits_ranked_by_softmax_scores(shift, E, k, G, tg):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,tg", [(32, 4, 8, 4), (256, 8, 8, 3), (96, 5, 1, 1)])
+def test_route_rows_of_the_lowest_float(scoring, E, k, G, tg):
+    """torch.finfo(float32).min is finite: a logit like any other, for a whole row, for a part of it
+    and beside the largest float."""
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    L = _logits(65, E, 37)
+    L[::4] = low
+    L[1::4, : E // 2] = low
+    L[2::4] = -math.inf
+    L[2::4, 1::3] = low
+    L[3, 1:] = low
+    L[3, 0] = high
+    L[7] = high
+    bias = 0.02 * _logits(1, E, 41)[0]
+    for b in (None, bias):
+        for group_score in ("top2", "max"):
+            for renorm in (True, False):
+                kw = dict(scoring=scoring, n_groups=G, topk_groups=tg, group_score=group_score, renormalize=renorm)
+                if scoring == "softmax":
+                    _check(L, k, b, **kw)
+                    continue
+                # Two sigmoids of the lowest float are more than one: float64 cannot hold either, but both
+                # at -700, where nothing else ranks below or between and the weights are still 0.
+                ids, w = ml.route(L.to(DEV), k, bias=None if b is None else b.to(DEV), **kw)
+                near = torch.where(L == low, -700.0, L).numpy()
+                rid, rw = _reference(near, k, bias=None if b is None else b.numpy(), **kw)
+                np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+                assert np.all(np.abs(w.cpu().numpy() - rw) <= _weight_bound(near, k, rw))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [17, 2100])
 def test_route_strided_and_unaligned_rows(T):
     wide = torch.randn(T, 77, device=DEV)
