@@ -341,11 +341,14 @@ __device__ __forceinline__ void lane_list(const RouteScoredArgs& a, const LaneEx
     }
     kept = rank < a.topk_groups;
     if constexpr (MODE == kByScore32) {
-      const float gf = (float)gs;
-      const float last = over_lanes<L, 0>(rank == a.topk_groups - 1 ? gf : -kBig, most);
-      const float next = over_lanes<L, 0>(rank == a.topk_groups ? gf : -kBig, most);
-      // twice an fp32 choice's error for each of up to two summands
-      unsure |= gs > kLeast && next > -1e38f && last - next < 0x1p-18f + 0x1p-20f * fabsf(last);
+      // Error of a group's sum: an fp32 choice's for each of up to two summands. It goes by their
+      // sizes, as biases of opposite signs may cancel in the sum. The groups are sure where the lowest
+      // bound of a kept one lies above the highest of the others.
+      const bool any = gs > kLeast;
+      const float gf = (float)gs, err = 0x1p-19f + 0x1p-22f * (fabsf((float)m1) + fabsf((float)second));
+      const float below = over_lanes<L, 0>(any && kept ? err - gf : -kBig, most);
+      const float above = over_lanes<L, 0>(any && !kept ? gf + err : -kBig, most);
+      unsure |= above > -kBig && below + above > 0.f;
     }
   }
 

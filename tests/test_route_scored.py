@@ -250,6 +250,22 @@ def test_route_rows_of_the_lowest_float(scoring, E, k, G, tg):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [5, 4099])
+def test_route_group_sums_whose_biases_cancel(scoring, T):
+    """Two experts a group with biases 4096 and -4096: a group's score is the sum of its two scores,
+    but a choice value in fp32 is off by up to 2^-12."""
+    G, tg = 16, 5
+    L = _logits(T, 2 * G, 43)
+    bias = torch.tensor([4096.0, -4096.0]).repeat(G)
+    l = L.double()
+    s = (torch.softmax(l, 1) if scoring == "softmax" else torch.sigmoid(l)).view(T, G, 2)
+    for v in (s.sum(2), s[:, :, 0], s[:, :, 1]):  # (told apart by 2^-42 of 4096, 1e-9)
+        assert v.sort(1).values.diff(dim=1).min() > 4e-9
+    _check(L, tg, bias, scoring=scoring, n_groups=G, topk_groups=tg, group_score="top2")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [17, 2100])
 def test_route_strided_and_unaligned_rows(T):
     wide = torch.randn(T, 77, device=DEV)
