@@ -58,12 +58,12 @@ void* dense(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef 
   return t.data_ptr();
 }
 
-// Row stride of a matrix whose rows are dense but may lie apart (of a single row: its length, as
-// torch's stride of it means nothing).
+// Row stride of a matrix whose rows are dense but may lie apart. A single row's is its length: nobody
+// steps by torch's stride of it, which may be anything (a sequence's length for its last position).
 int64_t row_stride(const Tensor& t, const char* name) {
   const int64_t rows = t.size(0), cols = t.size(1);
   if (cols > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "%s: the elements of a row must be adjacent%s", name);
-  if (rows <= 1) return cols > t.stride(0) ? cols : t.stride(0);
+  if (rows <= 1) return cols;
   if (t.stride(0) < cols) refuse(PyExc_ValueError, "%s: rows must not overlap%s", name);
   return t.stride(0);
 }

@@ -138,6 +138,35 @@ def test_linear_strided_rows(T, K, N, act, w):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,w", [("none", "bf16"), ("swiglu", "bf16"), ("none", "e4m3")])
+def test_linear_one_row_of_any_stride(act, w):
+    """The stride of a single row is never stepped: one token of a long sequence for x, the residual
+    and y, rows of buffers whose width is no multiple of 16 bytes, a W of one row."""
+    K, N = 512, 96
+    x, W, scale, b, r = _inputs(1, K, N, act, w, 61)
+
+    def last(t):  # the last position of a sequence [1][S][n]
+        n = t.shape[1]
+        seq = torch.zeros(1, (1 << 22) // n + 2, n, dtype=t.dtype, device=DEV)
+        seq[:, -1] = t
+        assert seq[:, -1].stride(0) >= 1 << 22
+        return seq[:, -1]
+
+    def odd(t):  # the first row of a buffer of odd width
+        wide = torch.zeros(3, t.shape[1] + 3, dtype=t.dtype, device=DEV)
+        wide[:1, :t.shape[1]] = t
+        return wide[:1, :t.shape[1]]
+
+    for place in (last, odd):
+        y = place(torch.zeros(1, N, dtype=BF, device=DEV))
+        assert ml.linear(place(x), W, w_scale=scale, bias=b, act=act, residual=place(r), y=y) is y
+        _compare(y, x, W, scale, b, act, r)
+    if act == "none":
+        one = ml.linear(place(x), place(W[:1]), w_scale=None if scale is None else scale[:1], bias=b[:1])
+        _compare(one, x, W[:1], None if scale is None else scale[:1], b[:1], act, None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,N", [(5, 96), (150, 96), (1100, 1000)])
 def test_linear_onto_its_residual(T, N):
     x, W, _, b, r = _inputs(T, 512, N, "gelu", "bf16", 21)

@@ -266,6 +266,20 @@ def test_route_group_sums_whose_biases_cancel(scoring, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_one_token_of_any_stride(bias):
+    """The stride of a single row is never stepped: the last position of a long sequence, a view
+    whose stride is less than its row."""
+    E, k = 64, 6
+    b = 0.1 * _logits(1, E, 47)[0] if bias else None
+    long = torch.empty(1, 1 << 16, E, device=DEV)
+    long[:, -1] = _logits(1, E, 53).to(DEV)
+    assert long[:, -1].stride(0) >= 1 << 22
+    _check(long[:, -1], k, b)
+    _check(torch.as_strided(long, (1, E), (3, 1), ((1 << 16) - 1) * E), k, b)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [17, 2100])
 def test_route_strided_and_unaligned_rows(T):
     wide = torch.randn(T, 77, device=DEV)
