@@ -442,7 +442,8 @@ def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y
     x [T][K] bf16; W [N][K] bf16, or uint8 E4M3 codes with w_scale [N] float32; bias [N] and
     residual [T][N] bf16. act: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu", for which
     W (w_scale, bias) has 2 N rows, gate then up. Rows of x, W, residual and y may lie apart (x
-    and W rows 16-byte aligned). y may be the residual; over another input it is refused.
+    and W rows 16-byte aligned). y may be the residual; a y or a workspace in use that shares a byte
+    with another argument is refused.
     sgmv(x, A, B, adapter_ids, y) adds a batch's adapters to a projection without an activation."""
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")

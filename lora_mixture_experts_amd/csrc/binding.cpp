@@ -12,11 +12,15 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "byte_ranges.h"
 #include "moelora.h"
 
 namespace {
 
 using at::Tensor;
+using moelora::Bytes;
+using moelora::dense_bytes;
+using moelora::overlap;
 
 struct Refused {};  // a Python exception is set
 PyObject* out_of_memory = nullptr;  // torch.OutOfMemoryError
@@ -158,13 +162,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Whether two tensors are sure to share bytes: the same start, or ranges of dense ones that meet
-// (column slices of one buffer interleave without sharing any).
-bool overlap(const Tensor& a, const Tensor& b) {
-  if (!a.numel() || !b.numel()) return false;
-  const char *p = (const char*)a.data_ptr(), *q = (const char*)b.data_ptr();
-  return p == q || (a.is_contiguous() && b.is_contiguous() && p < q + b.nbytes() && q < p + a.nbytes());
+// (a matrix whose rows row_stride has accepted, or a contiguous tensor)
+Bytes bytes_of(const Tensor& t) {
+  if (t.dim() != 2 || t.is_contiguous()) return dense_bytes(t.data_ptr(), (int64_t)t.nbytes());
+  const int64_t e = (int64_t)t.element_size();
+  return {(const char*)t.data_ptr(), t.numel() ? t.size(0) : 0, t.size(1) * e, t.stride(0) * e};
 }
+Bytes bytes_of(PyObject* o) { return o == Py_None ? Bytes{nullptr, 0, 0, 0} : bytes_of(THPVariable_Unpack(o)); }
 
 // linear(x, W, w_scale, bias, act, residual, y, workspace) -> y
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -208,15 +212,22 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     d.y_stride = row_stride(y, "y");
     if (a[6] != Py_None) {
+      const Bytes out = bytes_of(y);
       const bool in_place = residual == y.data_ptr() && (T == 1 || d.residual_stride == d.y_stride);
-      if (overlap(y, x) || overlap(y, W) || (residual && !in_place && overlap(y, *tensor_of(a[5], "residual"))))
-        refuse(PyExc_ValueError, "%s overlaps an input%s", "y");
+      for (const int i : {0, 1, 2, 3, 5})
+        if (overlap(out, bytes_of(a[i])) && !(i == 5 && in_place))
+          refuse(PyExc_ValueError, "%s overlaps an input%s", "y");
     }
     Tensor ws;
     if (a[7] != Py_None) {
       ws = *tensor_of(a[7], "workspace");
       check(ws, "workspace", at::kByte, ws.sizes(), dev);
       if (!ws.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous%s", "workspace");
+      const size_t need = moe_lora_linear_workspace_size(&d);
+      const Bytes used = dense_bytes(ws.data_ptr(), std::min((int64_t)need, ws.numel()));
+      bool shares = overlap(used, bytes_of(y));
+      for (const int i : {0, 1, 2, 3, 5}) shares |= overlap(used, bytes_of(a[i]));
+      if (shares) refuse(PyExc_ValueError, "%s overlaps another argument%s", "workspace");
     } else if (const size_t need = moe_lora_linear_workspace_size(&d)) {
       ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
     }

@@ -357,3 +357,47 @@ def test_linear_refuses_outputs_over_inputs():
     assert torch.equal(ml.linear(x, W, y=y), want)
     one = buf[:1, :64].clone()
     assert torch.equal(ml.linear(x[:1], W, residual=one, y=one), one)
+
+
+@pytest.mark.gpu
+def test_linear_refuses_every_shared_byte():
+    """y in column slices that meet an input's, over a bias, a scale or a workspace in use; slices that
+    share no byte are taken, whatever their strides."""
+    buf = torch.randn(16, 256, device=DEV).to(BF)
+    W = torch.randn(64, 64, device=DEV).to(BF)
+    x = buf[:8, :64]
+    want = ml.linear(x, W)
+    for y in (buf[:8, 32:96], buf[1:9, :64], buf[:8, 63:127], buf[::2, 8:72], buf.view(-1)[:8 * 320].view(8, 320)[:, 64:128]):
+        with pytest.raises(ValueError, match="overlaps"):
+            ml.linear(x, W, y=y)
+    for y in (buf[:8, 64:128], buf[8:, :64], buf[::2, 64:128], buf[1::2, 192:]):
+        assert torch.equal(ml.linear(x, W, y=y), want)
+    r = torch.randn(8, 64, device=DEV).to(BF)
+    with pytest.raises(ValueError, match="overlaps"):
+        ml.linear(r, W, residual=buf[:8, :64], y=buf[:8, 8:72])
+    line = torch.zeros(8 * 64 + 64, dtype=BF, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        ml.linear(r, W, bias=line[448:512], y=line[:512].view(8, 64))
+    codes = torch.zeros(64, 64, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        ml.linear(r, codes, w_scale=line.view(torch.float32)[224:288], y=line[:512].view(8, 64))
+    assert torch.equal(ml.linear(r, W, bias=line[512:], y=line[:512].view(8, 64)), ml.linear(r, W))
+
+    # a workspace counts where the call uses one, and as far as it does
+    T, K, N = 100, 8192, 64
+    x, W, _, b, _ = _inputs(T, K, N, "none", "bf16", 71, True, False)
+    d = ml.LinearDims(T, K, N, 0, 0, K, K, N, N)
+    need = ml.lib().moe_lora_linear_workspace_size(ctypes.byref(d))
+    assert need > 0
+    ws = torch.empty(need + T * N * 2, dtype=torch.uint8, device=DEV)
+    behind = ws[need:].view(BF).view(T, N)
+    assert torch.equal(ml.linear(x, W, bias=b, y=behind, workspace=ws), ml.linear(x, W, bias=b))
+    within = ws[need - 16:need - 16 + T * N * 2].view(BF).view(T, N)
+    with pytest.raises(ValueError, match="overlaps"):
+        ml.linear(x, W, bias=b, y=within, workspace=ws)
+    with pytest.raises(ValueError, match="overlaps"):
+        ml.linear(x, W, bias=b, workspace=x.view(-1).view(torch.uint8))
+    few, part = x[:1, :512], W[:, :512]
+    d = ml.LinearDims(1, 512, N, 0, 0, 512, K, N, N)
+    assert ml.lib().moe_lora_linear_workspace_size(ctypes.byref(d)) == 0
+    assert torch.equal(ml.linear(few, part, bias=b, workspace=x.view(-1).view(torch.uint8)), ml.linear(few, part, bias=b))
