@@ -295,8 +295,8 @@ typedef struct {
  * token_mask uint8 [T] or NULL (0: a row of padding, whose logits are not read and whose slots all
  * stay empty), topk_ids int32 [T][topk], topk_w f32 [T][topk], token_flags int32 [T] or NULL (1
  * where a logit of the token was not finite). Device pointers, caller-owned, aligned to their
- * elements; no workspace. topk_ids and topk_w go into moe_lora_forward_topk. Asynchronous on
- * `stream`. Errors: MOELORA_EINVAL_DIMS for a field out of the ranges above, MOELORA_ENULL,
+ * elements, no output over an input or another output; no workspace. topk_ids and topk_w go into
+ * moe_lora_forward_topk. Asynchronous on `stream`. Errors: MOELORA_EINVAL_DIMS for a field out of the ranges above, MOELORA_ENULL,
  * MOELORA_EALIGN, MOELORA_EDEVICE, MOELORA_EHIP. With T = 0 nothing is enqueued. */
 int moe_lora_route(const float *logits, const float *bias, const uint8_t *token_mask,
                    const moe_lora_router *r, int32_t *topk_ids, float *topk_w,

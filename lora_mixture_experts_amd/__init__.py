@@ -392,7 +392,8 @@ def route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_groups: i
     n_groups, topk_groups, group_score ("max" or "top2"): only the best groups' experts are
     chosen from; renormalize: weights over the sum of the chosen; token_mask [T] bool: False for
     rows of padding. Empty slots hold expert -1 and weight 0. token_flags [T] int32, when given,
-    receives 1 where a token's logits were not all finite."""
+    receives 1 where a token's logits were not all finite. An output that shares a byte with another
+    argument is refused."""
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {sorted(SCORINGS)}")
     if group_score not in GROUP_SCORES:

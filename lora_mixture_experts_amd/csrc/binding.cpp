@@ -77,6 +77,14 @@ int32_t size32(int64_t v, const char* name) {
   return (int32_t)v;
 }
 
+// (a matrix whose rows row_stride has accepted, or a contiguous tensor)
+Bytes bytes_of(const Tensor& t) {
+  if (t.dim() != 2 || t.is_contiguous()) return dense_bytes(t.data_ptr(), (int64_t)t.nbytes());
+  const int64_t e = (int64_t)t.element_size();
+  return {(const char*)t.data_ptr(), t.numel() ? t.size(0) : 0, t.size(1) * e, t.stride(0) * e};
+}
+Bytes bytes_of(PyObject* o) { return o == Py_None ? Bytes{nullptr, 0, 0, 0} : bytes_of(THPVariable_Unpack(o)); }
+
 // call(stream) with GPU `device` current, on torch's current stream of it.
 template <class F>
 int on_device(int device, F call) {
@@ -149,6 +157,13 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* bias = dense(a[3], "bias", at::kFloat, {E}, dev);
     const void* mask = dense(a[9], "token_mask", at::kBool, {T}, dev);
     void* flags = dense(a[12], "token_flags", at::kInt, {T}, dev);
+    for (const int out : {10, 11, 12}) {
+      if (a[out] == Py_None) continue;
+      for (const int other : {0, 3, 9, 10, 11, 12})
+        if (other != out && overlap(bytes_of(a[out]), bytes_of(a[other])))
+          refuse(PyExc_ValueError, "%s overlaps another argument%s",
+                 out == 10 ? "topk_ids" : out == 11 ? "topk_w" : "token_flags");
+    }
     const int rc = on_device(dev, [&](void* stream) {
       return moe_lora_route((const float*)logits.data_ptr(), (const float*)bias, (const uint8_t*)mask, &r,
                             (int32_t*)ids.data_ptr(), (float*)w.data_ptr(), (int32_t*)flags, stream);
@@ -161,14 +176,6 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return out;
   });
 }
-
-// (a matrix whose rows row_stride has accepted, or a contiguous tensor)
-Bytes bytes_of(const Tensor& t) {
-  if (t.dim() != 2 || t.is_contiguous()) return dense_bytes(t.data_ptr(), (int64_t)t.nbytes());
-  const int64_t e = (int64_t)t.element_size();
-  return {(const char*)t.data_ptr(), t.numel() ? t.size(0) : 0, t.size(1) * e, t.stride(0) * e};
-}
-Bytes bytes_of(PyObject* o) { return o == Py_None ? Bytes{nullptr, 0, 0, 0} : bytes_of(THPVariable_Unpack(o)); }
 
 // linear(x, W, w_scale, bias, act, residual, y, workspace) -> y
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {

@@ -365,3 +365,29 @@ def test_route_refuses_choices_before_it_allocates():
     for k in (33, 2 ** 31 - 1, 0, -1):
         with pytest.raises(ml.MoeLoraError):
             ml.route(logits, k)
+
+
+@pytest.mark.gpu
+def test_route_refuses_outputs_over_arguments():
+    T, E, k = 6, 64, 4
+    buf = torch.randn(T, 3 * E, device=DEV)
+    logits, bias = buf[:, :E], torch.zeros(E + T * k, device=DEV)
+    want = ml.route(logits, k)
+    mask = torch.ones(4 * T + T, dtype=torch.uint8, device=DEV)
+    bad = [dict(topk_w=buf.view(-1)[E - 1:E - 1 + T * k].view(T, k)), dict(topk_w=bias[E - 1:E - 1 + T * k].view(T, k)),
+           dict(topk_ids=buf.view(torch.int32).view(-1)[:T * k].view(T, k)),
+           dict(token_flags=buf.view(torch.int32).view(-1)[-2 * E - 1:-2 * E - 1 + T]),
+           dict(token_flags=mask[:4 * T].view(torch.int32), token_mask=mask[4 * T - 1:5 * T - 1].view(torch.bool))]
+    both = torch.zeros(T * k + 4, device=DEV)
+    bad.append(dict(topk_w=both[:T * k].view(T, k), topk_ids=both.view(torch.int32)[4:].view(T, k)))
+    bad.append(dict(topk_w=both[:T * k].view(T, k), token_flags=both.view(torch.int32)[:T]))
+    for kw in bad:
+        with pytest.raises(ValueError, match="overlaps"):
+            ml.route(logits, k, bias=bias[:E], **kw)
+    rest = torch.zeros(2 * T * k + T, dtype=torch.int32, device=DEV)  # side by side
+    ids, w = ml.route(logits, k, bias=bias[:E], token_mask=mask[4 * T:].view(torch.bool),
+                      topk_ids=rest[:T * k].view(T, k), topk_w=rest[T * k:2 * T * k].view(torch.float32).view(T, k),
+                      token_flags=mask[:4 * T].view(torch.int32))
+    assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+    ids, w = ml.route(logits, k, topk_w=buf.view(-1)[E:E + T * k].view(T, k))  # between two rows
+    assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
