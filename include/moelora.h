@@ -350,6 +350,19 @@ typedef struct {
  * are not supported). 256-byte aligned, no initialisation needed. Host-only. */
 size_t moe_lora_linear_workspace_size(const moe_lora_linear_dims *d);
 
+/* The kernel a projection of these sizes takes, for inspection and tests (the choice is this
+ * library's, no page defines it): with T <= 64, the one that streams the weights through registers, or
+ * one that stages tiles of tile_rows tokens x tile_cols weight rows in LDS, with k_groups groups of
+ * wavefronts that share a tile's reduction and `splits` workgroups that share it (their sums meet in
+ * the workspace). residual_stride is not looked at. Host-only. Returns MOELORA_OK, the error that
+ * moe_lora_linear gives for the sizes, or MOELORA_ENULL. */
+typedef struct {
+  int32_t streamed; /* 1: weights streamed; the next three fields are 0, splits is 1 */
+  int32_t tile_rows, tile_cols, k_groups, splits;
+} moe_lora_linear_plan_info;
+
+int moe_lora_linear_plan(const moe_lora_linear_dims *d, moe_lora_linear_plan_info *out);
+
 /* The projection above. x bf16, W bf16 or E4M3 codes (both 16-byte aligned), w_scale f32 (E4M3
  * only, else NULL), bias bf16 or NULL, residual bf16 or NULL, y bf16 (aligned to their elements).
  * y may be the residual itself (the same pointer and stride), and no other overlap of y with an

@@ -25,7 +25,7 @@ EXPORTS = ("moe_lora_workspace_size", "moe_lora_forward", "moe_lora_forward_time
            "moe_lora_debug_status", "moe_lora_sgmv_workspace_size", "moe_lora_sgmv",
            "moe_lora_router_logits", "moe_lora_forward_routed", "moe_lora_workspace_layout",
            "moe_lora_route", "moe_lora_forward_topk", "moe_lora_linear", "moe_lora_linear_workspace_size",
-           "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
+           "moe_lora_linear_plan", "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
 N_STAGES = 7
 STAGES = ("route", "align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
 
@@ -60,6 +60,10 @@ class Router(ctypes.Structure):
 class LinearDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "in_features", "out_features", "act", "w_type")] + [
         (n, ctypes.c_int64) for n in ("x_stride", "w_stride", "y_stride", "residual_stride")]
+
+
+class LinearPlanInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("streamed", "tile_rows", "tile_cols", "k_groups", "splits")]
 
 
 SCORINGS = {"softmax": 0, "sigmoid": 1}
@@ -116,6 +120,8 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_forward_topk.restype = ctypes.c_int
         L.moe_lora_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDims)]
         L.moe_lora_linear_workspace_size.restype = ctypes.c_size_t
+        L.moe_lora_linear_plan.argtypes = [ctypes.POINTER(LinearDims), ctypes.POINTER(LinearPlanInfo)]
+        L.moe_lora_linear_plan.restype = ctypes.c_int
         L.moe_lora_linear.argtypes = [P, P, P, P, P, ctypes.POINTER(LinearDims), P, P, ctypes.c_size_t, P]
         L.moe_lora_linear.restype = ctypes.c_int
         L.moe_lora_strerror.argtypes = [ctypes.c_int]
@@ -434,6 +440,17 @@ def forward_topk(x, topk_ids, topk_w, W1, W2, A1, B1, A2, B2, adapter_ids, *, W1
         _dense(y, "y", bf, (T, h), dev), _dense(workspace, "workspace", torch.uint8, workspace.shape, dev),
         workspace.numel())
     return y
+
+
+def linear_plan(T: int, in_features: int, out_features: int, act: str = "none", e4m3: bool = False) -> dict:
+    """Kernel, tile and splits that linear takes for these sizes (moe_lora_linear_plan), host-only."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    d = LinearDims(T, in_features, out_features, ACTIVATIONS[act], 1 if e4m3 else 0, in_features, in_features,
+                   out_features, out_features)
+    out = LinearPlanInfo()
+    _check(lib().moe_lora_linear_plan(ctypes.byref(d), ctypes.byref(out)), "moe_lora_linear_plan")
+    return {n: getattr(out, n) for n, _ in LinearPlanInfo._fields_}
 
 
 def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y=None,

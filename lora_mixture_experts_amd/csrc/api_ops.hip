@@ -149,6 +149,20 @@ size_t moe_lora_linear_workspace_size(const moe_lora_linear_dims* d) {
   return linear_workspace(d, plan_linear(d));
 }
 
+int moe_lora_linear_plan(const moe_lora_linear_dims* d, moe_lora_linear_plan_info* out) {
+  const int rc = validate_linear(d, false);
+  if (rc != MOELORA_OK) return rc;
+  if (!out) return MOELORA_ENULL;
+  const LinearPlan p = plan_linear(d);
+  if (!p.stream && p.bm == 0) return MOELORA_EINVAL_DIMS;
+  out->streamed = p.stream ? 1 : 0;
+  out->tile_rows = p.stream ? 0 : p.bm;
+  out->tile_cols = p.stream ? 0 : p.bn;
+  out->k_groups = p.stream ? 0 : p.kg;
+  out->splits = p.splits;
+  return MOELORA_OK;
+}
+
 int moe_lora_linear(const void* x, const void* W, const float* w_scale, const void* bias,
                     const void* residual, const moe_lora_linear_dims* d, void* y, void* workspace,
                     size_t workspace_bytes, void* stream) {

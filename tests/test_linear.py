@@ -275,6 +275,50 @@ def test_linear_empty_batch():
     assert ml.linear(torch.empty(0, 16, dtype=BF, device=DEV), W).shape == (0, 24)
 
 
+# Sizes that take each tile of the tiled kernel, with and without splits of the reduction: (T, K, N, tile
+# rows, tile columns, split), the same for bf16 and E4M3. Rows, columns and K are no multiple of a tile or
+# of a step; the last of each list reads more than 128 MB of bf16 weights in one row tile.
+FORMS = [(131, 784, 203, 64, 64, False), (67, 4112, 257, 64, 64, True), (257, 528, 4203, 64, 128, False),
+         (40, 4112, 4203, 64, 128, True), (1500, 528, 1301, 128, 128, False), (2051, 3088, 131, 128, 128, True),
+         (3000, 528, 4203, 256, 256, False), (3000, 4112, 1301, 256, 256, True), (40, 4112, 17003, 64, 128, False)]
+SWIGLU_FORMS = [(131, 784, 203, 64, 64, False), (67, 4112, 257, 64, 64, True), (403, 1040, 2101, 64, 128, False),
+                (40, 4112, 4203, 64, 128, True), (257, 528, 4203, 128, 128, False), (67, 3088, 2050, 128, 128, True),
+                (3000, 528, 2101, 256, 256, False), (193, 8208, 4203, 256, 256, True), (40, 4112, 8501, 64, 128, False)]
+
+
+def _assert_form(T, K, N, rows, cols, split, act, w):
+    p = ml.linear_plan(T, K, N, act, w == "e4m3")
+    groups = {(64, 64): 4, (64, 128): 2}.get((rows, cols), 1)
+    assert (p["streamed"], p["tile_rows"], p["tile_cols"], p["k_groups"]) == (0, rows, cols, groups)
+    assert (p["splits"] > 1) == split
+
+
+@pytest.mark.parametrize("w", ["bf16", "e4m3"])
+def test_linear_plan_of_every_form(w):
+    """The sizes that the tests of the tiled kernel's forms are made for still take them."""
+    for form in FORMS:
+        for act in ("none", "relu", "silu", "gelu", "gelu_tanh"):
+            _assert_form(*form, act, w)
+    for form in SWIGLU_FORMS:
+        _assert_form(*form, "swiglu", w)
+    one = ml.linear_plan(1, 4096, 4096, e4m3=w == "e4m3")
+    assert one == dict(streamed=1, tile_rows=0, tile_cols=0, k_groups=0, splits=1)
+
+
+def test_linear_plan_refuses():
+    for bad in (dict(T=-1), dict(in_features=508), dict(out_features=1 << 22), dict(T=(1 << 30) - 1, out_features=1 << 20)):
+        f = dict(T=100, in_features=512, out_features=64)
+        f.update(bad)
+        with pytest.raises(ml.MoeLoraError) as e:
+            ml.linear_plan(**f)
+        assert e.value.code == ml.EINVAL_DIMS
+    with pytest.raises(ValueError):
+        ml.linear_plan(1, 16, 16, "tanh")
+    d = ml.LinearDims(100, 512, 64, 0, 0, 512, 512, 64, 64)
+    assert ml.lib().moe_lora_linear_plan(ctypes.byref(d), None) == ml.ENULL
+    assert ml.lib().moe_lora_linear_plan(None, ctypes.byref(ml.LinearPlanInfo())) == ml.ENULL
+
+
 # ----------------------------------------------------------------------------- refusals (CPU)
 
 FIELDS = dict(T=100, in_features=512, out_features=64, act=0, w_type=0, x_stride=512, w_stride=512, y_stride=64,
