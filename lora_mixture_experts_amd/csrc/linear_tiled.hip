@@ -197,6 +197,9 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
           for (int e = 0; n + e < a.N; ++e) to[e] = v[e];
         }
       }
+      // (the next 32 rows go where other lanes of the wavefront have just read: LDS accesses of a wavefront
+      // keep their order, the barrier keeps the compiler from changing it)
+      if (KG == 1) __builtin_amdgcn_wave_barrier();
       continue;
     }
     if (!GATED && KG == 1 && a.act != kActNone) {

@@ -319,6 +319,23 @@ def test_linear_plan_refuses():
     assert ml.lib().moe_lora_linear_plan(None, ctypes.byref(ml.LinearPlanInfo())) == ml.ENULL
 
 
+def _acts(forms, acts, split):
+    return [(*f, a) for f in forms for a in acts if f[-1] == split]
+
+
+ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,K,N,rows,cols,split,act", _acts(FORMS, ACTS, True) + _acts(SWIGLU_FORMS, ("swiglu",), True))
+def test_linear_split_forms(T, K, N, rows, cols, split, act, w):
+    """Splits of every tile (a wavefront of the 256 x 256 one writes its sums 32 rows at a time through
+    the same LDS), and every activation in the launch that adds them."""
+    _assert_form(T, K, N, rows, cols, split, act, w)
+    _check(T, K, N, act, w)
+
+
 # ----------------------------------------------------------------------------- refusals (CPU)
 
 FIELDS = dict(T=100, in_features=512, out_features=64, act=0, w_type=0, x_stride=512, w_stride=512, y_stride=64,
