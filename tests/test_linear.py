@@ -336,6 +336,54 @@ def test_linear_split_forms(T, K, N, rows, cols, split, act, w):
     _check(T, K, N, act, w)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,K,N,rows,cols,split,act", _acts(FORMS, ACTS, False) + _acts(SWIGLU_FORMS, ("swiglu",), False))
+def test_linear_whole_forms(T, K, N, rows, cols, split, act, w):
+    """Every tile without splits: several turns of the LDS ring, a partial last step, each activation."""
+    _assert_form(T, K, N, rows, cols, split, act, w)
+    _check(T, K, N, act, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,rows,cols,split,act", _acts(FORMS, ("silu",), False) + _acts(FORMS, ("none",), True)
+                         + _acts(SWIGLU_FORMS, ("swiglu",), False) + _acts(SWIGLU_FORMS, ("swiglu",), True))
+@pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True)])
+def test_linear_forms_without_operands(T, K, N, rows, cols, split, act, bias, residual):
+    _assert_form(T, K, N, rows, cols, split, act, "bf16")
+    _check(T, K, N, act, "bf16", bias, residual)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,rows,cols,split,act", _acts(FORMS, ("gelu",), False) + _acts(FORMS, ("gelu",), True)
+                         + _acts(SWIGLU_FORMS, ("swiglu",), False) + _acts(SWIGLU_FORMS, ("swiglu",), True))
+def test_linear_forms_onto_the_residual(T, K, N, rows, cols, split, act):
+    """y in place of the residual, inside a wider buffer whose other columns stay."""
+    _assert_form(T, K, N, rows, cols, split, act, "bf16")
+    x, W, _, b, r = _inputs(T, K, N, act, "bf16", 81)
+    wide = torch.full((T, N + 5), 7.0, dtype=BF, device=DEV)
+    y = wide[:, 3:3 + N]
+    y.copy_(r)
+    assert ml.linear(x, W, bias=b, act=act, residual=y, y=y) is y
+    _compare(y, x, W, None, b, act, r)
+    assert (wide[:, :3] == 7).all() and (wide[:, 3 + N:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 131, 3000])
+def test_linear_decodes_every_e4m3_code(T):
+    """All 256 codes, one a weight row, against torch's decoding: NaN codes give NaN, in their column only."""
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV)
+    W = torch.zeros(256, 528, dtype=torch.uint8, device=DEV)
+    W[:, 517] = codes
+    x = torch.zeros(T, 528, dtype=BF, device=DEV)
+    x[:, 517] = 1.0
+    y = ml.linear(x, W, w_scale=torch.ones(256, device=DEV)).float()
+    want = codes.view(torch.float8_e4m3fn).float().expand(T, 256)
+    assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.isnan(want).sum() == 2 * T
+    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(want))
+
+
 # ----------------------------------------------------------------------------- refusals (CPU)
 
 FIELDS = dict(T=100, in_features=512, out_features=64, act=0, w_type=0, x_stride=512, w_stride=512, y_stride=64,
