@@ -281,7 +281,7 @@ int moe_lora_workspace_layout(const moe_lora_dims *d, int32_t topk, moe_lora_lay
 #define MOELORA_GROUP_MAX 0
 #define MOELORA_GROUP_TOP2 1
 typedef struct {
-  int32_t T, n_experts, topk; /* T in [0, 2^26); n_experts in [1, 1024]; topk in [1, min(n_experts, 16)] */
+  int32_t T, n_experts, topk; /* T in [0, 2^26 - 4]; n_experts in [1, 1024]; topk in [1, min(n_experts, 16)] */
   int32_t scoring;            /* MOELORA_SCORE_* */
   int32_t n_groups;           /* divides n_experts, at most 64 */
   int32_t topk_groups;        /* in [1, n_groups]; topk <= topk_groups * n_experts / n_groups */

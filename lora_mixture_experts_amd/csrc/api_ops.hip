@@ -16,7 +16,8 @@ constexpr int64_t kMaxRowStride = (int64_t)1 << 22;  // a workgroup's (up to 256
 
 int validate_router(const moe_lora_router* r) {
   if (!r) return MOELORA_ENULL;
-  if (r->T < 0 || r->T >= (1 << 26) || r->n_experts < 1 || r->n_experts > kMaxExperts) return MOELORA_EINVAL_DIMS;
+  // (four tokens in a workgroup of 256: a launch holds fewer than 2^32 threads)
+  if (r->T < 0 || r->T > (1 << 26) - 4 || r->n_experts < 1 || r->n_experts > kMaxExperts) return MOELORA_EINVAL_DIMS;
   if (r->topk < 1 || r->topk > r->n_experts || r->topk > kMaxTopk) return MOELORA_EINVAL_DIMS;
   if (r->scoring != MOELORA_SCORE_SOFTMAX && r->scoring != MOELORA_SCORE_SIGMOID)
     return MOELORA_EINVAL_DIMS;

@@ -336,6 +336,14 @@ def test_route_refuses_fields_out_of_range(bad):
     assert _call(**bad) == ml.EINVAL_DIMS
 
 
+def test_route_refuses_more_tokens_than_a_launch_holds():
+    """Four tokens a workgroup of 256 threads, fewer than 2^32 threads a launch."""
+    odd = [0x10002, 0x20000, 0x30000, 0x40000, 0x50000, 0x60000]  # (refused next, whatever the sizes)
+    assert _call(odd, T=(1 << 26) - 4, n_experts=1024, logits_stride=1024) == ml.EALIGN
+    for T in ((1 << 26) - 3, (1 << 26) - 1):
+        assert _call(odd, T=T, n_experts=1024, logits_stride=1024) == ml.EINVAL_DIMS
+
+
 def test_route_refuses_pointers():
     base = [0x10000, 0x20000, 0x30000, 0x40000, 0x50000, 0x60000]
     for i in (0, 3, 4):
