@@ -32,7 +32,7 @@ int validate_dims(const moe_lora_dims* d, int32_t topk) {
   // every index the kernels form in 32 bits must fit
   const int64_t P = (int64_t)d->T * topk;
   if (P + (int64_t)d->n_experts * kMaxBM >= ((int64_t)1 << 30)) return MOELORA_EINVAL_DIMS;
-  if ((int64_t)d->n_experts * (d->n_adapters + 1) >= ((int64_t)1 << 28)) return MOELORA_EINVAL_DIMS;
+  if ((int64_t)d->n_experts * ((int64_t)d->n_adapters + 1) >= ((int64_t)1 << 28)) return MOELORA_EINVAL_DIMS;
   // x and the intermediate activations are read with 32-bit buffer offsets (< 2 GiB each)
   // (the activations are checked against the capacity of the path a call takes, once planned)
   if ((int64_t)d->T * d->hidden * 2 >= ((int64_t)1 << 31)) return MOELORA_EINVAL_DIMS;
@@ -694,7 +694,7 @@ int check_forward(const void* x, const float* router_logits, const void* W_route
 int check_given_dims(const moe_lora_dims* d, int32_t topk) {
   const int rc = validate_dims(d, topk);
   if (rc != MOELORA_OK) return rc;
-  return (int64_t)d->n_experts * (d->n_adapters + 1) + 1 < ((int64_t)1 << 28) ? MOELORA_OK
+  return (int64_t)d->n_experts * ((int64_t)d->n_adapters + 1) + 1 < ((int64_t)1 << 28) ? MOELORA_OK
                                                                               : MOELORA_EINVAL_DIMS;
 }
 
