@@ -264,7 +264,8 @@ int moe_lora_workspace_layout(const moe_lora_dims *d, int32_t topk, moe_lora_lay
  * is finite (others, and with a bias those whose bias is not finite, are never chosen):
  *   score    s_e = softmax over those experts, or 1 / (1 + exp(-logit_e));
  *   choice   c_e = s_e + bias_e. Without a bias the experts rank by their logits, which order
- *            them as the scores do (by the scores where groups are ranked by a sum of two);
+ *            them as the scores do (by the scores with MOELORA_GROUP_TOP2 and more than one group,
+ *            kept or not: there scores closer than 2^-42 of their size are a tie);
  *   groups   n_groups runs of n_experts / n_groups consecutive experts. A group ranks by its
  *            largest choice value, or by the sum of its two largest (of the one, where a group has
  *            one expert to choose); the topk_groups best keep their experts, ties to the lower
@@ -336,7 +337,8 @@ int moe_lora_forward_topk(const void *x, const int32_t *topk_ids, const float *t
 #define MOELORA_W_E4M3 1
 typedef struct {
   int32_t T, in_features, out_features; /* T in [0, 2^30); in_features a positive multiple of 8
-                                           (E4M3: of 16); out_features in [1, 2^30) */
+                                           (E4M3: of 16); out_features at least 1 (both under 2^22,
+                                           as the strides are) */
   int32_t act;    /* MOELORA_ACT_* */
   int32_t w_type; /* MOELORA_W_BF16, or MOELORA_W_E4M3: OCP E4M3 codes with one scale per row, as
                      in moe_lora_forward_fp8 */

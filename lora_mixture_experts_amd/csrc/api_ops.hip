@@ -52,7 +52,8 @@ int validate_linear(const moe_lora_linear_dims* d, bool residual) {
 
 // Kernel, tile and reduction splits of a call, from its sizes alone: the least of an estimate in
 // microseconds, fitted to 7 100 shapes (T 1 to 6000, K 128 to 14 000, N 64 to 14 000, both weight
-// types, with and without SwiGLU) on which every kernel, tile and split was timed. Its choice is on
+// types, with and without SwiGLU) on which every kernel, tile and split was timed, in calls one after
+// another over three sets of tensors. Its choice is on
 // average 1% above the fastest, in nine shapes of ten at most 2%, in 99 of 100 at most 18%; without
 // the streaming kernel the choice is 8% above on average (18% up to 64 tokens), without the 64 x 64,
 // 64 x 128, 128 x 128 or 256 x 256 tile 6%, 3%, 4% or 2.5%. bm = 0 without `stream`: more tiles than
@@ -135,7 +136,7 @@ int moe_lora_route(const float* logits, const float* bias, const uint8_t* token_
   a.topk_groups = r->topk_groups;
   a.group_top2 = r->group_score == MOELORA_GROUP_TOP2;
   a.scoring = r->scoring;
-  // (groups that all stay are no groups: their scores are not needed)
+  // (the order by scores also holds where every group stays and no sum of two is formed)
   a.by_score = bias || (a.group_top2 && r->n_groups > 1) ? 1 : 0;
   a.renormalize = r->renormalize;
   a.scale = r->scale;
@@ -197,10 +198,12 @@ int moe_lora_linear(const void* x, const void* W, const float* w_scale, const vo
   a.K = d->in_features;
   a.rows = (int64_t)d->out_features * (d->act == MOELORA_ACT_SWIGLU ? 2 : 1);
   a.act = d->act;
-  // One row tile reads every weight once. Where they are too many to be found in the 256 MB last-level
-  // cache by the next call, the hint keeps them from evicting what can be (180 MB of bf16: one token 42.5
-  // -> 39.0 us, 64 tokens 47.9 -> 45.1); smaller ones stay there between calls, and the hint would lose
-  // that (33 MB: 10.9 -> 12.0). An E4M3 row gives half a line a step, which the hint drops.
+  // One row tile reads every weight once. The hint keeps them from evicting what can be found in the 256 MB
+  // last-level cache, and from being found there by the next call. Too many to be kept: one token with
+  // 180 MB of bf16 42.5 -> 39.0 us, 64 tokens 47.9 -> 45.1. Fewer gain from it where other work has emptied
+  // the cache (64 tokens, 67 MB: 36.2 -> 25.8 us; 90 MB: 47.5 -> 31.2) and lose where they are called again
+  // at once (20.6 -> 23.6; 25.3 -> 29.0): they go without. An E4M3 row gives half a line a step, which the
+  // hint drops.
   a.stream_w = !w8 && d->T <= kLinearStreamTokens && a.rows * a.K * 2 >= ((int64_t)128 << 20);
   a.part = (float*)workspace;
   a.splits = 1;

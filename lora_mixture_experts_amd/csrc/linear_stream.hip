@@ -10,12 +10,14 @@
 // row and of a token row. The wavefronts share nothing and wait for nobody until their partial
 // tiles meet in LDS, where they are added in wavefront order (the result does not depend on timing).
 // Two register sets alternate: a chunk's loads are in flight during the MFMAs of the one before
-// (three or four sets, two chunks a step and 32 columns a workgroup measured 2 to 40% slower). What
-// the epilogue adds is loaded first, so that it costs no round trip at the end.
+// (three or four sets, two chunks a step and 32 columns a workgroup measured 2 to 40% slower on weights
+// that the last call had left in the last-level cache). What the epilogue adds is loaded first, so that
+// it costs no round trip at the end.
 //
-// Measured: 4096 x 4096 bf16, one token 8.3 us (4.0 TB/s), 16 tokens 10.2. From some 80 MB of
-// weights on the tiled kernel, whose workgroups read longer pieces of more rows, is the faster
-// one (one token, 8541 x 8768: 31 us against 45).
+// Measured: 4096 x 4096 bf16, one token 8.3 us (4.0 TB/s) called again and again, 16 tokens 10.2; one
+// token with the caches emptied before the call 15.1 (2.2 TB/s: 4 KB a wavefront in flight do not cover
+// the latency of HBM). From some 80 MB of weights on the tiled kernel, whose workgroups read longer
+// pieces of more rows, is the faster one (one token, 8541 x 8768: 31 us against 45).
 #include "common.h"
 #include "kernels.h"
 #include "linear.h"

@@ -7,8 +7,10 @@
 // [gate i .. | up i ..] for the same outputs i, so a lane holds both.
 //
 // What bounds it: the MFMAs in 256 x 256 tiles (a 64-wide step of a lone tile takes 1.05 us for
-// 0.9 us of MFMAs); in smaller tiles what one CU can draw through its L1, 80 to 90 GB/s whatever the
-// ring's depth (64 x 128 tiles: 0.53 us for two steps). So small batches spread over the CUs, first in
+// 0.9 us of MFMAs); in smaller bf16 tiles what one CU can draw through its L1, 80 to 90 GB/s whatever the
+// ring's depth (64 x 128 tiles: 0.53 us for two steps of 24 KB); in E4M3 ones the latency of a step, which
+// carries 16 KB and takes as long (50 GB/s). A round of tiles costs another 2 to 9 us that nothing
+// overlaps: the fill of the ring and the epilogue. So small batches spread over the CUs, first in
 // the workgroup: KG groups of wavefronts, each with a ring of its own, take an equal share of the
 // reduction and their sums meet in the epilogue's LDS (256 x 2048 x 1536, 96 tiles: 15.7 us with
 // one group, 12.5 with four; a second launch would cost 4 us). Where the tiles would still leave
