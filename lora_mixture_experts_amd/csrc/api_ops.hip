@@ -53,11 +53,10 @@ int validate_linear(const moe_lora_linear_dims* d, bool residual) {
 // Kernel, tile and reduction splits of a call, from its sizes alone: the least of an estimate in
 // microseconds, fitted to 7 100 shapes (T 1 to 6000, K 128 to 14 000, N 64 to 14 000, both weight
 // types, with and without SwiGLU) on which every kernel, tile and split was timed, in calls one after
-// another over three sets of tensors. Its choice is on
-// average 1% above the fastest, in nine shapes of ten at most 2%, in 99 of 100 at most 18%; without
-// the streaming kernel the choice is 8% above on average (18% up to 64 tokens), without the 64 x 64,
-// 64 x 128, 128 x 128 or 256 x 256 tile 6%, 3%, 4% or 2.5%. bm = 0 without `stream`: more tiles than
-// a launch can hold.
+// another over three sets of tensors. Its choice is on average 1% above the fastest, in nine shapes of
+// ten at most 2%, in 99 of 100 at most 18%; without the streaming kernel the choice is 8% above on
+// average (18% up to 64 tokens), without the 64 x 64, 64 x 128, 128 x 128 or 256 x 256 tile 6%, 3%, 4%
+// or 2.5%. bm = 0 without `stream`: more tiles than a launch can hold.
 LinearPlan plan_linear(const moe_lora_linear_dims* d) {
   const bool gated = d->act == MOELORA_ACT_SWIGLU, w8 = d->w_type == MOELORA_W_E4M3;
   const double rows = (double)d->out_features * (gated ? 2 : 1), wb = w8 ? 1.0 : 2.0;
