@@ -3,6 +3,7 @@ the result, and the fp32 sum's error (K additions of at most 2^-24 of the sum of
 through the activation, with 2^-18 of the value for the fp32 epilogue (exponential, division)."""
 import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -267,6 +268,38 @@ def test_linear_weights_past_4_gib(T):
     assert (y[:, :rows // 2 - 300] == 0).all()
     y2 = ml.linear(x, W, act="swiglu")
     _compare(y2[:, -300:], x, torch.cat([tail, tail]), None, None, "swiglu", None)
+
+
+@pytest.mark.gpu
+def test_linear_and_route_from_two_threads():
+    """Two threads, each on a stream of its own, split and whole forms: the same bits as alone."""
+    x, W, _, b, r = _inputs(100, 2064, 131, "silu", "bf16", 91)
+    assert ml.linear_plan(100, 2064, 131, "silu")["splits"] > 1
+    x2, W2, s2, b2, _ = _inputs(300, 1040, 515, "none", "e4m3", 92, True, False)
+    logits, bias = torch.randn(700, 96, device=DEV), 0.1 * torch.randn(96, device=DEV)
+
+    def calls():
+        ids, w = ml.route(logits, 6, scoring="sigmoid", bias=bias, n_groups=8, topk_groups=3, group_score="top2")
+        return ml.linear(x, W, bias=b, act="silu", residual=r), ml.linear(x2, W2, w_scale=s2, bias=b2), ids, w
+
+    want = calls()
+    torch.cuda.synchronize()
+    right = []
+
+    def work():
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(200):
+                got = calls()
+                side.synchronize()
+                right.append(all(torch.equal(g, v) for g, v in zip(got, want)))
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(right) == 400 and all(right)
 
 
 @pytest.mark.gpu
