@@ -375,6 +375,77 @@ int moe_lora_linear(const void *x, const void *W, const float *w_scale, const vo
                     const void *residual, const moe_lora_linear_dims *d, void *y, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/* Dense projection with a batch's adapters inside its epilogue (page "vLLM MoE LoRA SageMaker Bedrock",
+ * section "O Papel da Multi-LoRA": xW + xAB with W frozen; page "Punica: Multi-Tenant LoRA Serving",
+ * proposed method: one batch, a different adapter for each request):
+ *   z[t][q] = sum_k x[t][k] A[a][q][k],  a = adapter_ids[t]
+ *   y[t][n] = act(w_scale[n] * sum_k x[t][k] W[n][k] + sum_q z[t][q] B[a][n][q] + bias[n]) + residual[t][n]
+ * The adapters' term comes before the bias and the activation, as the model's own projections need it
+ * (moe_lora_sgmv adds it behind a finished projection). A token with a = -1 has no such term. z is fp32
+ * and enters the second product with some 16 bits; everything else as in moe_lora_linear. SwiGLU: B has 2
+ * out_features rows as W has, one A serves both halves. */
+typedef struct {
+  moe_lora_linear_dims linear; /* as in moe_lora_linear, T under 2^24 */
+  int32_t n_adapters; /* at least 1, under 2^28 */
+  int32_t rank;       /* 8, 16, 32 or 64 */
+} moe_lora_linear_lora_dims;
+
+/* Bytes of device workspace moe_lora_linear_lora needs (0 for sizes that are not supported): z, the
+ * adapters of every 32 tokens, the sums of a split reduction. 256-byte aligned, no initialisation needed.
+ * Host-only. */
+size_t moe_lora_linear_lora_workspace_size(const moe_lora_linear_lora_dims *d);
+
+/* moe_lora_linear_plan for moe_lora_linear_lora. Host-only. */
+int moe_lora_linear_lora_plan(const moe_lora_linear_lora_dims *d, moe_lora_linear_plan_info *out);
+
+/* The projection above. A bf16 [n_adapters][rank][in_features] and B bf16 [n_adapters][W's rows][rank],
+ * dense and 16-byte aligned; adapter_ids int32 [T], in [-1, n_adapters): an id outside acts as -1 and sets
+ * MOELORA_FLAG_ADAPTER_RANGE (moe_lora_debug_status on this workspace). An adapter's infinities and NaNs
+ * reach the tokens that carry it and no others. Everything else (x, W, w_scale, bias, residual, y over the
+ * residual, errors) as in moe_lora_linear. */
+int moe_lora_linear_lora(const void *x, const void *W, const float *w_scale, const void *bias,
+                         const void *residual, const void *A, const void *B, const int32_t *adapter_ids,
+                         const moe_lora_linear_lora_dims *d, void *y, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* The norms around a block (the layer, or another block of the model; page "vLLM MoE LoRA SageMaker
+ * Bedrock", section "Entendendo os Modelos MoE": the layer's outputs are aggregated, and the model goes on
+ * with them; no page fixes the norms):
+ *   b[t]   = y[t], or with post_weight Norm(y[t]; post_weight, post_bias)
+ *   s[t]   = residual_scale * residual[t] + branch_scale * g[t] * b[t]
+ *   out[t] = Norm(s[t]; weight, bias)
+ *   Norm(v; w, c) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * w + c; MOELORA_NORM_RMS: without the
+ *            mean in it.
+ * In fp32 (out takes s before its rounding), each output rounded once. A row whose sum of squares passes the
+ * largest fp32 number is out of the range of this function. */
+#define MOELORA_NORM_RMS 0
+#define MOELORA_NORM_LAYER 1
+#define MOELORA_GATE_NONE 0     /* g = 1 */
+#define MOELORA_GATE_TOKEN 1    /* g f32 [T] */
+#define MOELORA_GATE_SIGMOID 2  /* 1 / (1 + e^-g), g f32 [T] */
+#define MOELORA_GATE_FEATURES 3 /* g bf16 [T] rows of hidden; gate_stride 0: one row for every token */
+typedef struct {
+  int32_t T, hidden; /* T in [0, 2^30); hidden in [1, 32768] */
+  int32_t norm;      /* MOELORA_NORM_* */
+  int32_t gate;      /* MOELORA_GATE_* */
+  float eps;         /* finite, not negative */
+  float residual_scale, branch_scale; /* finite */
+  /* elements between two rows, at least hidden (gate_stride may be 0) and under 2^40, of the tensors
+   * given (others are ignored) */
+  int64_t y_stride, residual_stride, gate_stride, sum_stride, out_stride;
+} moe_lora_block_norm_dims;
+
+/* The function above. y bf16 [T][hidden], or NULL for s = residual_scale * residual (then gate and the
+ * post norm's vectors are NULL too); residual bf16; gate as d->gate says, else NULL; post_weight, post_bias,
+ * weight, bias bf16 [hidden] or NULL (no bias without its weight); sum (s) bf16 or NULL where nobody needs
+ * it; out bf16, NULL if and only if weight is. One of sum and out at least. Tensors aligned to their elements. sum
+ * or out may be y or the residual itself (the same pointer and stride); no other overlap of an output with an
+ * argument is allowed. Asynchronous on `stream`; no workspace, allocates nothing. With T = 0 nothing is
+ * enqueued and no pointer is inspected. */
+int moe_lora_block_norm(const void *y, const void *residual, const void *gate, const void *post_weight,
+                        const void *post_bias, const void *weight, const void *bias,
+                        const moe_lora_block_norm_dims *d, void *sum, void *out, void *stream);
+
 /* Text for a return code (the MOELORA_E* codes above; no page defines them). Never NULL; the
  * string is static and owned by the library. */
 const char *moe_lora_strerror(int code);

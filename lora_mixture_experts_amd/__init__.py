@@ -3,8 +3,8 @@
 Thin ctypes binding over libmoelora.so (include/moelora.h). Every step of the layer runs in
 the library's HIP kernels; this module only checks tensor shapes, allocates outputs and the
 workspace with torch when the caller does not pass them, and hands raw device pointers and
-torch's current HIP stream to the C ABI. For route and linear, whose kernels take a few
-microseconds, a compiled module (csrc/binding.cpp) does the same. There is no fallback: without
+torch's current HIP stream to the C ABI. For the operators whose kernels take a few microseconds
+(route, linear, linear_lora, block_norm) a compiled module (csrc/binding.cpp) does the same. There is no fallback: without
 the built library or a gfx950 device every call raises.
 """
 from __future__ import annotations
@@ -25,7 +25,8 @@ EXPORTS = ("moe_lora_workspace_size", "moe_lora_forward", "moe_lora_forward_time
            "moe_lora_debug_status", "moe_lora_sgmv_workspace_size", "moe_lora_sgmv",
            "moe_lora_router_logits", "moe_lora_forward_routed", "moe_lora_workspace_layout",
            "moe_lora_route", "moe_lora_forward_topk", "moe_lora_linear", "moe_lora_linear_workspace_size",
-           "moe_lora_linear_plan", "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
+           "moe_lora_linear_plan", "moe_lora_linear_lora", "moe_lora_linear_lora_workspace_size",
+           "moe_lora_linear_lora_plan", "moe_lora_block_norm", "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
 N_STAGES = 7
 STAGES = ("route", "align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
 
@@ -62,6 +63,16 @@ class LinearDims(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("x_stride", "w_stride", "y_stride", "residual_stride")]
 
 
+class LinearLoraDims(ctypes.Structure):
+    _fields_ = [("linear", LinearDims), ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+class BlockNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "hidden", "norm", "gate")] + [
+        (n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale")] + [
+        (n, ctypes.c_int64) for n in ("y_stride", "residual_stride", "gate_stride", "sum_stride", "out_stride")]
+
+
 class LinearPlanInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("streamed", "tile_rows", "tile_cols", "k_groups", "splits")]
 
@@ -69,6 +80,8 @@ class LinearPlanInfo(ctypes.Structure):
 SCORINGS = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
+
+NORMS = {"rms": 0, "layer": 1}
 
 _lib = None
 _compiled = None
@@ -124,6 +137,15 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_linear_plan.restype = ctypes.c_int
         L.moe_lora_linear.argtypes = [P, P, P, P, P, ctypes.POINTER(LinearDims), P, P, ctypes.c_size_t, P]
         L.moe_lora_linear.restype = ctypes.c_int
+        L.moe_lora_linear_lora_workspace_size.argtypes = [ctypes.POINTER(LinearLoraDims)]
+        L.moe_lora_linear_lora_workspace_size.restype = ctypes.c_size_t
+        L.moe_lora_linear_lora_plan.argtypes = [ctypes.POINTER(LinearLoraDims), ctypes.POINTER(LinearPlanInfo)]
+        L.moe_lora_linear_lora_plan.restype = ctypes.c_int
+        L.moe_lora_linear_lora.argtypes = [P, P, P, P, P, P, P, P, ctypes.POINTER(LinearLoraDims), P, P,
+                                           ctypes.c_size_t, P]
+        L.moe_lora_linear_lora.restype = ctypes.c_int
+        L.moe_lora_block_norm.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(BlockNormDims), P, P, P]
+        L.moe_lora_block_norm.restype = ctypes.c_int
         L.moe_lora_strerror.argtypes = [ctypes.c_int]
         L.moe_lora_strerror.restype = ctypes.c_char_p
         L.moe_lora_debug_status.argtypes = [P, ctypes.c_size_t, P, ctypes.POINTER(ctypes.c_uint32)]
@@ -462,13 +484,65 @@ def linear(x, W, *, w_scale=None, bias=None, act: str = "none", residual=None, y
     W (w_scale, bias) has 2 N rows, gate then up. Rows of x, W, residual and y may lie apart (x
     and W rows 16-byte aligned). y may be the residual; a y or a workspace in use that shares a byte
     with another argument is refused.
-    sgmv(x, A, B, adapter_ids, y) adds a batch's adapters to a projection without an activation."""
+    sgmv(x, A, B, adapter_ids, y) adds a batch's adapters to a projection without an activation,
+    linear_lora takes them inside the epilogue."""
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
     out = (_compiled or _native()).linear(x, W, w_scale, bias, ACTIVATIONS[act], residual, y, workspace)
     if type(out) is int:
         raise MoeLoraError(out, "moe_lora_linear")
     return out
+
+
+def linear_lora(x, W, A, B, adapter_ids, *, w_scale=None, bias=None, act: str = "none", residual=None, y=None,
+                workspace=None) -> torch.Tensor:
+    """Dense projection with a batch's adapters inside its epilogue (moe_lora_linear_lora), bf16 [T][N]:
+    y[t] = act(x[t] W^T + (x[t] A_a^T) B_a^T + bias) + residual[t], a = adapter_ids[t] (-1: none).
+
+    A [nA][r][K] and B [nA][rows of W][r] bf16, contiguous, rank r 8, 16, 32 or 64; adapter_ids [T]
+    int32. The rest as in linear. debug_status(workspace) of a workspace given here tells of adapter ids
+    out of range."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    out = (_compiled or _native()).linear_lora(x, W, w_scale, bias, ACTIVATIONS[act], residual, y, workspace, A, B,
+                                               adapter_ids)
+    if type(out) is int:
+        raise MoeLoraError(out, "moe_lora_linear_lora")
+    return out
+
+
+def linear_lora_plan(T: int, in_features: int, out_features: int, n_adapters: int, rank: int, act: str = "none",
+                     e4m3: bool = False) -> dict:
+    """linear_plan for linear_lora (moe_lora_linear_lora_plan), host-only."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    d = LinearLoraDims(LinearDims(T, in_features, out_features, ACTIVATIONS[act], 1 if e4m3 else 0, in_features,
+                                  in_features, out_features, out_features), n_adapters, rank)
+    out = LinearPlanInfo()
+    _check(lib().moe_lora_linear_lora_plan(ctypes.byref(d), ctypes.byref(out)), "moe_lora_linear_lora_plan")
+    return {n: getattr(out, n) for n, _ in LinearPlanInfo._fields_}
+
+
+def block_norm(y, residual, weight=None, *, bias=None, post_weight=None, post_bias=None, gate=None,
+               sigmoid_gate: bool = False, residual_scale: float = 1.0, branch_scale: float = 1.0,
+               norm: str = "rms", eps: float = 1e-6, total=None, out=None):
+    """The norms around a block (moe_lora_block_norm): (total, out), bf16 [T][h], of what the block gave,
+    y [T][h], and the residual stream [T][h] (bf16, rows may lie apart):
+    total = residual_scale * residual + branch_scale * gate * b, b = y or, with post_weight [h], its norm;
+    out = the norm of total (before its rounding) with weight [h].
+
+    norm: "rms" or "layer", both with an optional bias [h]; gate: None, [T] float32 (through a sigmoid with
+    sigmoid_gate) or [T][h] bf16 (an expanded row is read as one). Without weight out is None; with y None
+    total is residual_scale * residual and only written where it is given. total and out may be y or the
+    residual; an output that shares other bytes with an argument is refused."""
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}")
+    pair = (_compiled or _native()).block_norm(y, residual, gate, 1 if sigmoid_gate else 0, post_weight, post_bias,
+                                               weight, bias, NORMS[norm], eps, residual_scale, branch_scale, total,
+                                               out)
+    if type(pair) is int:
+        raise MoeLoraError(pair, "moe_lora_block_norm")
+    return pair
 
 
 def forward_fp8(x, router_logits, W1q, W1_scale, W2q, W2_scale, A1, B1, A2, B2, adapter_ids,

@@ -1,5 +1,5 @@
 // Compiled half of the Python binding for the operators whose kernels take a few microseconds
-// (moe_lora_route, moe_lora_linear): checks of torch tensors, outputs and workspaces from torch's
+// (moe_lora_route, moe_lora_linear, moe_lora_linear_lora, moe_lora_block_norm): checks of torch tensors, outputs and workspaces from torch's
 // allocator, torch's current stream, one call of the C ABI. As attribute reads and ctypes conversions in
 // Python the same took 6 us of a 10 us call; here 1 us.
 //
@@ -178,15 +178,18 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // linear(x, W, w_scale, bias, act, residual, y, workspace) -> y
+// linear_lora(.., A, B, adapter_ids) -> y
+template <bool LORA>
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (n != 8) refuse(PyExc_TypeError, "%s takes 8 arguments%s", "linear");
+    if (n != (LORA ? 11 : 8)) refuse(PyExc_TypeError, "%s takes another number of arguments%s", "linear");
     const Tensor &x = *tensor_of(a[0], "x"), &W = *tensor_of(a[1], "W");
     if (x.dim() != 2 || W.dim() != 2) refuse(PyExc_ValueError, "%s must be [T][K] and W [N][K]%s", "x");
     const int64_t T = x.size(0), K = x.size(1), rows = W.size(0);
     const int dev = x.is_cuda() ? x.get_device() : -1;
     const bool w8 = a[2] != Py_None;
-    moe_lora_linear_dims d;
+    moe_lora_linear_lora_dims dims;
+    moe_lora_linear_dims& d = dims.linear;
     d.act = (int32_t)PyLong_AsLong(a[4]);
     if (d.act == -1 && PyErr_Occurred()) throw Refused{};
     const bool gated = d.act == MOELORA_ACT_SWIGLU;
@@ -196,6 +199,24 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(W, "W", w8 ? at::kByte : at::kBFloat16, {rows, K}, dev);
     const void* scale = dense(a[2], "w_scale", at::kFloat, {rows}, dev);
     const void* bias = dense(a[3], "bias", at::kBFloat16, {rows}, dev);
+    const void *A = nullptr, *B = nullptr, *ids = nullptr;
+    if (LORA) {
+      const Tensor& ta = *tensor_of(a[8], "A");
+      if (ta.dim() != 3) refuse(PyExc_ValueError, "%s must be [n_adapters][rank][K]%s", "A");
+      const int64_t nA = ta.size(0), r = ta.size(1);
+      A = dense(a[8], "A", at::kBFloat16, {nA, r, K}, dev);
+      tensor_of(a[9], "B");
+      B = dense(a[9], "B", at::kBFloat16, {nA, rows, r}, dev);
+      tensor_of(a[10], "adapter_ids");
+      ids = dense(a[10], "adapter_ids", at::kInt, {T}, dev);
+      dims.n_adapters = size32(nA, "n_adapters");
+      dims.rank = size32(r, "rank");
+    }
+    const auto workspace_size = [&] {
+      return LORA ? moe_lora_linear_lora_workspace_size(&dims) : moe_lora_linear_workspace_size(&d);
+    };
+    constexpr int inputs[] = {0, 1, 2, 3, 5, 8, 9, 10};
+    constexpr int n_inputs = LORA ? 8 : 5;
     d.T = size32(T, "T");
     d.in_features = size32(K, "K");
     d.out_features = size32(N, "N");
@@ -221,26 +242,33 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[6] != Py_None) {
       const Bytes out = bytes_of(y);
       const bool in_place = residual == y.data_ptr() && (T == 1 || d.residual_stride == d.y_stride);
-      for (const int i : {0, 1, 2, 3, 5})
+      for (int j = 0; j < n_inputs; ++j) {
+        const int i = inputs[j];
         if (overlap(out, bytes_of(a[i])) && !(i == 5 && in_place))
           refuse(PyExc_ValueError, "%s overlaps an input%s", "y");
+      }
     }
     Tensor ws;
     if (a[7] != Py_None) {
       ws = *tensor_of(a[7], "workspace");
       check(ws, "workspace", at::kByte, ws.sizes(), dev);
       if (!ws.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous%s", "workspace");
-      const size_t need = moe_lora_linear_workspace_size(&d);
+      const size_t need = workspace_size();
       const Bytes used = dense_bytes(ws.data_ptr(), std::min((int64_t)need, ws.numel()));
       bool shares = overlap(used, bytes_of(y));
-      for (const int i : {0, 1, 2, 3, 5}) shares |= overlap(used, bytes_of(a[i]));
+      for (int j = 0; j < n_inputs; ++j) shares |= overlap(used, bytes_of(a[inputs[j]]));
       if (shares) refuse(PyExc_ValueError, "%s overlaps another argument%s", "workspace");
-    } else if (const size_t need = moe_lora_linear_workspace_size(&d)) {
+    } else if (const size_t need = workspace_size()) {
       ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
     }
     const int rc = on_device(dev, [&](void* stream) {
+      void* const at = ws.defined() ? ws.data_ptr() : nullptr;
+      const size_t bytes = ws.defined() ? (size_t)ws.numel() : 0;
+      if (LORA)
+        return moe_lora_linear_lora(x.data_ptr(), W.data_ptr(), (const float*)scale, bias, residual, A, B,
+                                    (const int32_t*)ids, &dims, y.data_ptr(), at, bytes, stream);
       return moe_lora_linear(x.data_ptr(), W.data_ptr(), (const float*)scale, bias, residual, &d, y.data_ptr(),
-                             ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, stream);
+                             at, bytes, stream);
     });
     if (rc != MOELORA_OK) return PyLong_FromLong(rc);
     if (a[6] != Py_None) return Py_NewRef(a[6]);
@@ -248,8 +276,109 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// block_norm(y, residual, gate, sigmoid, post_weight, post_bias, weight, bias, norm, eps, residual_scale,
+//            branch_scale, sum, out) -> (sum, out)
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 14) refuse(PyExc_TypeError, "%s takes 14 arguments%s", "block_norm");
+    const Tensor& res = *tensor_of(a[1], "residual");
+    if (res.dim() != 2) refuse(PyExc_ValueError, "%s must be a [T][h] tensor%s", "residual");
+    const int64_t T = res.size(0), h = res.size(1);
+    const int dev = res.is_cuda() ? res.get_device() : -1;
+    moe_lora_block_norm_dims d = {};
+    d.T = size32(T, "T");
+    d.hidden = size32(h, "h");
+    auto matrix = [&](PyObject* o, const char* name, int64_t* stride) -> void* {
+      if (o == Py_None) return nullptr;
+      const Tensor& t = *tensor_of(o, name);
+      check(t, name, at::kBFloat16, {T, h}, dev);
+      *stride = row_stride(t, name);
+      return t.data_ptr();
+    };
+    auto number = [&](int i) {
+      const double v = PyFloat_AsDouble(a[i]);
+      if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+      return (float)v;
+    };
+    const void* residual = matrix(a[1], "residual", &d.residual_stride);
+    const void* y = matrix(a[0], "y", &d.y_stride);
+    const void* gate = nullptr;
+    Bytes gate_bytes = {nullptr, 0, 0, 0};
+    d.gate = MOELORA_GATE_NONE;
+    if (a[2] != Py_None) {
+      const Tensor& g = *tensor_of(a[2], "gate");
+      if (g.dim() == 1) {
+        gate = dense(a[2], "gate", at::kFloat, {T}, dev);
+        const long sigmoid = PyLong_AsLong(a[3]);
+        if (sigmoid == -1 && PyErr_Occurred()) throw Refused{};
+        d.gate = sigmoid ? MOELORA_GATE_SIGMOID : MOELORA_GATE_TOKEN;
+        gate_bytes = bytes_of(g);
+      } else {
+        check(g, "gate", at::kBFloat16, {T, h}, dev);
+        if (T > 1 && g.stride(0) == 0) {  // one row for every token
+          if (h > 1 && g.stride(1) != 1) refuse(PyExc_ValueError, "%s: the elements of a row must be adjacent%s", "gate");
+          gate_bytes = dense_bytes(g.data_ptr(), 2 * h);
+        } else {
+          d.gate_stride = row_stride(g, "gate");
+          gate_bytes = bytes_of(g);
+        }
+        gate = g.data_ptr();
+        d.gate = MOELORA_GATE_FEATURES;
+      }
+    }
+    const void* vectors[4];
+    const char* const names[] = {"post_weight", "post_bias", "weight", "bias"};
+    for (int i = 0; i < 4; ++i) vectors[i] = dense(a[4 + i], names[i], at::kBFloat16, {h}, dev);
+    const long norm = PyLong_AsLong(a[8]);
+    if (norm == -1 && PyErr_Occurred()) throw Refused{};
+    d.norm = (int32_t)norm;
+    d.eps = number(9);
+    d.residual_scale = number(10);
+    d.branch_scale = number(11);
+    Tensor sum, out;
+    if (a[12] != Py_None) sum = *tensor_of(a[12], "total");
+    else if (a[0] != Py_None) sum = at::empty({T, h}, res.options());
+    if (a[13] != Py_None) out = *tensor_of(a[13], "out");
+    else if (a[6] != Py_None) out = at::empty({T, h}, res.options());
+    for (const Tensor* t : {&sum, &out}) {
+      if (!t->defined()) continue;
+      const char* name = t == &sum ? "total" : "out";
+      check(*t, name, at::kBFloat16, {T, h}, dev);
+      int64_t& stride = t == &sum ? d.sum_stride : d.out_stride;
+      stride = row_stride(*t, name);
+      if (a[t == &sum ? 12 : 13] == Py_None) continue;
+      const Bytes b = bytes_of(*t);
+      bool shares = overlap(b, gate_bytes);
+      for (int i = 4; i < 8; ++i) shares |= overlap(b, bytes_of(a[i]));
+      for (int i = 0; i < 2; ++i) {
+        const bool same = a[i] != Py_None && THPVariable_Unpack(a[i]).data_ptr() == t->data_ptr() &&
+                          (T == 1 || (i ? d.residual_stride : d.y_stride) == stride);
+        shares |= overlap(b, bytes_of(a[i])) && !same;
+      }
+      const Tensor& other = t == &sum ? out : sum;
+      shares |= other.defined() && overlap(b, bytes_of(other));
+      if (shares) refuse(PyExc_ValueError, "%s overlaps another argument%s", name);
+    }
+    const int rc = on_device(dev, [&](void* stream) {
+      return moe_lora_block_norm(y, residual, gate, vectors[0], vectors[1], vectors[2], vectors[3], &d,
+                                 sum.defined() ? sum.data_ptr() : nullptr, out.defined() ? out.data_ptr() : nullptr,
+                                 stream);
+    });
+    if (rc != MOELORA_OK) return PyLong_FromLong(rc);
+    PyObject* pair = PyTuple_New(2);
+    if (!pair) return nullptr;
+    for (int i = 0; i < 2; ++i) {
+      Tensor& t = i ? out : sum;
+      PyTuple_SET_ITEM(pair, i, t.defined() ? THPVariable_Wrap(std::move(t)) : Py_NewRef(Py_None));
+    }
+    return pair;
+  });
+}
+
 PyMethodDef methods[] = {{"route", (PyCFunction)(void (*)(void))route, METH_FASTCALL, nullptr},
-                         {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, nullptr},
+                         {"linear", (PyCFunction)(void (*)(void))linear<false>, METH_FASTCALL, nullptr},
+                         {"linear_lora", (PyCFunction)(void (*)(void))linear<true>, METH_FASTCALL, nullptr},
+                         {"block_norm", (PyCFunction)(void (*)(void))block_norm, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

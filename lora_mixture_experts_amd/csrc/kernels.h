@@ -167,7 +167,31 @@ struct SgmvArgs {
   int N, r;
 };
 
-// Dense projection y = act(scale * (x W^T) + bias) + residual (moe_lora_linear). SwiGLU: W holds
+// Adapters of 32 consecutive tokens: the distinct ones among them, in the order of their first tokens,
+// and which tokens carry each.
+struct TokenAdapters {
+  int n;            // distinct adapters
+  int bad;          // 1 where an id was out of range (taken as none)
+  int pad[6];
+  int adapter[32];
+  uint32_t tokens[32];  // bit i: token i of the 32
+};
+
+// LoRA shrink of tokens in their own order: z = x A_a^T for the projection with adapters, and the
+// adapters of every 32 tokens.
+struct TokenShrinkArgs {
+  const uint16_t* X;  // [T] rows of K bf16, ldx apart
+  const uint16_t* A;  // [nA][r][K]
+  const int* adapter_ids;  // [T]
+  int64_t ldx;
+  int T, K, nA, r;
+  float* z;  // [T][r], rows without an adapter unwritten
+  TokenAdapters* groups;  // [ceil(T / 32)]
+  int slots;  // workgroups that share the adapters of 32 tokens
+};
+
+// Dense projection y = act(scale * (x W^T) + bias) + residual (moe_lora_linear), with adapters
+// act(scale * (x W^T) + z B_a^T + bias) + residual (moe_lora_linear_lora). SwiGLU: W holds
 // 2 N rows, gate then up.
 enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSwiglu = 5 };
 constexpr int kLinearStreamTokens = 64;  // token rows the weight-streaming kernel takes
@@ -187,12 +211,34 @@ struct LinearArgs {
   // tiled
   float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
   int splits, row_tiles, col_tiles;
+  // with adapters
+  const float* z;               // [T][r]
+  const uint16_t* B;            // [nA][rows][r]
+  const TokenAdapters* groups;  // [ceil(T / 32)]
+  int* flags;                   // [1]: the workspace's
+  int r;
 };
 struct LinearPlan {
   bool stream;
   int bm, bn, nst;  // tile and LDS stages
   int kg;           // groups of wavefronts that share a tile's reduction
   int splits;       // of the reduction
+};
+
+constexpr int kMaxNormHidden = 32768;
+// Norms around a block (moe_lora_block_norm). Rows of h bf16, ld* elements apart.
+struct BlockNormArgs {
+  const uint16_t* y;  // what the block gave, or nullptr
+  const uint16_t* residual;
+  const float* token_gate;  // [T], or nullptr
+  const uint16_t* gate;     // [T] rows, ldg (0: one row for all) apart, or nullptr
+  const uint16_t *post_weight, *post_bias;  // [h] or nullptr: y goes in as it is
+  const uint16_t *weight, *bias;            // [h]; weight nullptr: no second norm
+  uint16_t* sum;  // or nullptr
+  uint16_t* out;  // with weight
+  int64_t ldy, ldr, ldg, lds, ldo;
+  int T, h, layer, sigmoid;
+  float eps, residual_scale, branch_scale;
 };
 
 // Tile shape of the LDS-staged GEMM: nw wavefronts of WM x WN each; NST LDS stages of BK k.
@@ -233,6 +279,9 @@ hipError_t launch_tiled(const TiledConfig& c, bool gateup, const GemmArgs& a, hi
                         bool fp8 = false);
 hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t stream);
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream);
+hipError_t launch_linear_lora(const LinearPlan& p, const LinearArgs& a, hipStream_t stream);
 hipError_t launch_sgmv_expand(const SgmvArgs& a, int max_blocks, hipStream_t stream);
 // D parts: d_parts == nullptr: ksplit parts for every row; else d_parts[(row / part_rows) *
 // part_ncol + col / part_cols] parts (1 to 4) for the tile holding (row, col).

@@ -119,4 +119,27 @@ struct ScaleBias {
   }
 };
 
+// Eight values of a token's z (fp32) as one MFMA operand of the expand z B^T. z keeps some 16 bits: it
+// enters as two bf16, high and low = bf16(z - high), whose columns lie one after the other, so that the
+// reduction is 2 r long and each of B's columns is taken twice.
+__device__ __forceinline__ u32x4 z_operand(const float* z, bool low) {
+  const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = *reinterpret_cast<const f32x4*>(z + 4);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = i < 2 ? z0[2 * i] : z1[2 * i - 4], hi = i < 2 ? z0[2 * i + 1] : z1[2 * i - 3];
+    const uint32_t top = to_bf16x2(lo, hi);
+    w[i] = low ? to_bf16x2(lo - bf16_lo(top), hi - bf16_hi(top)) : top;
+  }
+  return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// The flag of moe_lora_debug_status for a call with adapters: one wavefront, once every group is written.
+__device__ __forceinline__ void report_adapter_range(const LinearArgs& a) {
+  bool bad = false;
+  for (int g = threadIdx.x & 63; g < (a.T + 31) / 32; g += 64) bad |= a.groups[g].bad != 0;
+  const bool any = __ballot(bad) != 0;
+  if ((threadIdx.x & 63) == 0) *a.flags = any ? 2 : 0;  // MOELORA_FLAG_ADAPTER_RANGE
+}
+
 }  // namespace moelora

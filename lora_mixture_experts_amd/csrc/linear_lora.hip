@@ -1,0 +1,153 @@
+// Dense projection with a batch's adapters inside its epilogue (moe_lora_linear_lora): the shrink of the
+// tokens, and the projection's kernels with the expand on their accumulators.
+//
+//   z[t][q] = sum_k x[t][k] A_a[q][k], a the token's adapter
+//   y[t][n] = act(scale[n] * sum_k x[t][k] W[n][k] + sum_q z[t][q] B_a[n][q] + bias[n]) + r[t][n]
+//
+// Page "vLLM MoE LoRA SageMaker Bedrock", section "O Papel da Multi-LoRA": the frozen product plus the
+// shrink and the expand; page "Punica: Multi-Tenant LoRA Serving", proposed method: one batch, a
+// different adapter for each of its requests. Two launches (three with a split reduction): every token's
+// z has to be whole before the first expand.
+#include "common.h"
+#include "kernels.h"
+#include "linear_stream.h"
+#include "linear_tiled.h"
+
+namespace moelora {
+
+namespace {
+constexpr int kShrinkWaves = 8;
+}
+
+// Shrink. A workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
+// index blockIdx.y, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (no
+// sort by adapter: the tokens of a prompt lie together anyway, and those of a decode batch are mostly of
+// different requests). 16x16x32 MFMAs with the rows of A on their A side and 16 tokens on their B side;
+// tokens without the adapter load zeros, which costs no traffic, and their sums are dropped. The eight
+// wavefronts take the 64-wide K chunks in turn, two in flight, and their sums meet in LDS in wavefront
+// order, in fp32.
+// NQ: 16-row tiles of A (rank 8 and 16: 1, 32: 2, 64: 4). NT: 16-token tiles.
+template <int NQ, int NT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenShrinkArgs a) {
+  constexpr int WK = kShrinkWaves;
+  const int lane = threadIdx.x & 63;
+  const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, kq = lane >> 4;
+  const int t0 = blockIdx.x * 32, K = a.K, r = a.r;
+
+  // the group's adapters, found by every wavefront for itself
+  const int given = lane < 32 && t0 + lane < a.T ? a.adapter_ids[t0 + lane] : -1;
+  const int ad = sanitize_adapter(given, a.nA);
+  const bool bad = __ballot(given != ad && given != -1) != 0;
+  TokenAdapters* const grp = a.groups + blockIdx.x;
+  const bool writes = blockIdx.y == 0 && wk == 0;
+
+  __shared__ f32x4 part[WK][NQ][NT][64];
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X + (int64_t)t0 * a.ldx, 0x7fffffffu);
+  uint32_t left = (uint32_t)__ballot(ad >= 0);
+  int n = 0;
+  while (left) {
+    const int one = __builtin_amdgcn_readlane(ad, __builtin_ctz(left));
+    const uint32_t who = (uint32_t)__ballot(ad == one) & left;
+    left &= ~who;
+    const int index = n++;
+    if (writes && lane == 0) {
+      grp->adapter[index] = one;
+      grp->tokens[index] = who;
+    }
+    if (index % a.slots != (int)blockIdx.y) continue;
+    const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.A + (int64_t)one * r * K, (uint32_t)((size_t)r * K * 2));
+    uint32_t ao[NQ], xo[NT];
+#pragma unroll
+    for (int c = 0; c < NQ; ++c) ao[c] = c * 16 + m < r ? (uint32_t)((size_t)(c * 16 + m) * K * 2) : kOutOfRange;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      xo[nt] = (who >> (nt * 16 + m)) & 1u ? (uint32_t)((nt * 16 + m) * a.ldx * 2) : kOutOfRange;
+    f32x4 acc[NQ][NT];
+#pragma unroll
+    for (int c = 0; c < NQ; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[c][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Set {
+      u32x4 w[NQ][2], x[NT][2];
+    };
+    auto load = [&](Set& s, int step) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = (step * WK + wk) * 64 + 32 * j + 8 * kq;
+        const bool in = k < K;
+#pragma unroll
+        for (int c = 0; c < NQ; ++c) s.w[c][j] = bufld16(ar, in ? ao[c] + (uint32_t)(k * 2) : kOutOfRange);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s.x[nt][j] = bufld16(xr, in ? xo[nt] + (uint32_t)(k * 2) : kOutOfRange);
+      }
+    };
+    auto compute = [&](const Set& s) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < NQ; ++c)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[c][nt] = mfma16(s.w[c][j], s.x[nt][j], acc[c][nt]);
+    };
+    const int nsteps = (K + 64 * WK - 1) / (64 * WK);
+    Set sa, sb;
+    load(sa, 0);
+    for (int i = 0; i < nsteps; i += 2) {  // (steps past the end load and add zeros)
+      load(sb, i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(sa);
+      __builtin_amdgcn_sched_barrier(0);
+      load(sa, i + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(sb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();  // (the sums of the adapter before have been read)
+#pragma unroll
+    for (int c = 0; c < NQ; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) part[wk][c][nt][lane] = acc[c][nt];
+    __syncthreads();
+    // lane: z columns 16 c + 4 kq .. + 3 of token nt * 16 + m
+    for (int i = wk; i < NQ * NT; i += WK) {
+      const int c = i / NT, nt = i % NT, q = 16 * c + 4 * kq;
+      f32x4 sum = part[0][c][nt][lane];
+#pragma unroll
+      for (int p = 1; p < WK; ++p) sum += part[p][c][nt][lane];
+      if (q < r && ((who >> (nt * 16 + m)) & 1u))
+        *reinterpret_cast<f32x4*>(a.z + ((int64_t)t0 + nt * 16 + m) * r + q) = sum;
+    }
+  }
+  if (writes && lane == 0) {
+    grp->n = n;
+    grp->bad = bad;
+  }
+}
+
+hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream) {
+  if (a.T <= 0) return hipSuccess;
+  if (a.slots < 1 || a.slots > 32 || a.K % 8 != 0) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((a.T + 31) / 32), (unsigned)a.slots), block(64 * kShrinkWaves);
+  const bool one = a.T <= 16;
+#define MOELORA_TOKEN_SHRINK(NQ_)                                                              \
+  if (one) hipLaunchKernelGGL((token_shrink_kernel<NQ_, 1>), grid, block, 0, stream, a);       \
+  else hipLaunchKernelGGL((token_shrink_kernel<NQ_, 2>), grid, block, 0, stream, a)
+  if (a.r == 8 || a.r == 16) {
+    MOELORA_TOKEN_SHRINK(1);
+  } else if (a.r == 32) {
+    MOELORA_TOKEN_SHRINK(2);
+  } else if (a.r == 64) {
+    MOELORA_TOKEN_SHRINK(4);
+  } else {
+    return hipErrorInvalidValue;
+  }
+#undef MOELORA_TOKEN_SHRINK
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_lora(const LinearPlan& p, const LinearArgs& a, hipStream_t stream) {
+  return p.stream ? launch_stream_form<true>(a, stream) : launch_tiled_form<true>(p, a, stream);
+}
+
+}  // namespace moelora
