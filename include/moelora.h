@@ -446,6 +446,28 @@ int moe_lora_block_norm(const void *y, const void *residual, const void *gate, c
                         const void *post_bias, const void *weight, const void *bias,
                         const moe_lora_block_norm_dims *d, void *sum, void *out, void *stream);
 
+/* Bytes of device workspace moe_lora_forward_few needs (0 for sizes that are not supported): the choices,
+ * the shrink outputs and the activations. 256-byte aligned, no initialisation needed. Host-only. */
+size_t moe_lora_few_workspace_size(const moe_lora_dims *d, int32_t topk);
+
+/* The layer for a few tokens, as a decode step of one or a few requests calls it (page "AWS SageMaker MoE
+ * kernel optimizations", second paragraph: single-token decode; page "vLLM MoE LoRA SageMaker Bedrock",
+ * section "Entendendo os Modelos MoE"): the function of moe_lora_forward (router_logits f32 [T][E] given,
+ * topk_ids and topk_w NULL) or of moe_lora_forward_topk (topk_ids int32 and topk_w f32 [T][topk] given,
+ * router_logits NULL), for T in [0, 16], in three launches and without a sorted layout. The activations
+ * between the two products keep some 16 bits (moe_lora_forward rounds them to bf16), so the results agree
+ * with moe_lora_forward's up to that rounding. W1_scale and W2_scale NULL: bf16 W1 and W2; both given:
+ * E4M3 codes and scales, as in moe_lora_forward_fp8. Layouts, supported sizes (but T), flags and errors as
+ * there; an expert's and an adapter's infinities and NaNs reach the tokens that chose them and no others.
+ * Pointers 16-byte aligned (scales, router_logits, topk_ids, topk_w and adapter_ids to 4 bytes). Results do
+ * not depend on timing. */
+int moe_lora_forward_few(const void *x, const float *router_logits, const int32_t *topk_ids,
+                         const float *topk_w, const void *W1, const float *W1_scale, const void *W2,
+                         const float *W2_scale, const void *A1, const void *B1, const void *A2,
+                         const void *B2, const int32_t *adapter_ids, int32_t topk,
+                         const moe_lora_dims *d, void *y, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
 /* Text for a return code (the MOELORA_E* codes above; no page defines them). Never NULL; the
  * string is static and owned by the library. */
 const char *moe_lora_strerror(int code);

@@ -4,7 +4,7 @@ Thin ctypes binding over libmoelora.so (include/moelora.h). Every step of the la
 the library's HIP kernels; this module only checks tensor shapes, allocates outputs and the
 workspace with torch when the caller does not pass them, and hands raw device pointers and
 torch's current HIP stream to the C ABI. For the operators whose kernels take a few microseconds
-(route, linear, linear_lora, block_norm) a compiled module (csrc/binding.cpp) does the same. There is no fallback: without
+(route, linear, linear_lora, block_norm, forward_few) a compiled module (csrc/binding.cpp) does the same. There is no fallback: without
 the built library or a gfx950 device every call raises.
 """
 from __future__ import annotations
@@ -26,7 +26,8 @@ EXPORTS = ("moe_lora_workspace_size", "moe_lora_forward", "moe_lora_forward_time
            "moe_lora_router_logits", "moe_lora_forward_routed", "moe_lora_workspace_layout",
            "moe_lora_route", "moe_lora_forward_topk", "moe_lora_linear", "moe_lora_linear_workspace_size",
            "moe_lora_linear_plan", "moe_lora_linear_lora", "moe_lora_linear_lora_workspace_size",
-           "moe_lora_linear_lora_plan", "moe_lora_block_norm", "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
+           "moe_lora_linear_lora_plan", "moe_lora_block_norm", "moe_lora_forward_few",
+           "moe_lora_few_workspace_size", "moe_lora_forward_noalloc", "moe_lora_probe_read", "moe_lora_probe_mfma")
 N_STAGES = 7
 STAGES = ("route", "align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
 
@@ -146,6 +147,10 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_linear_lora.restype = ctypes.c_int
         L.moe_lora_block_norm.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(BlockNormDims), P, P, P]
         L.moe_lora_block_norm.restype = ctypes.c_int
+        L.moe_lora_few_workspace_size.argtypes = [D, i32]
+        L.moe_lora_few_workspace_size.restype = ctypes.c_size_t
+        L.moe_lora_forward_few.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, i32, D, P, P, ctypes.c_size_t, P]
+        L.moe_lora_forward_few.restype = ctypes.c_int
         L.moe_lora_strerror.argtypes = [ctypes.c_int]
         L.moe_lora_strerror.restype = ctypes.c_char_p
         L.moe_lora_debug_status.argtypes = [P, ctypes.c_size_t, P, ctypes.POINTER(ctypes.c_uint32)]
@@ -543,6 +548,23 @@ def block_norm(y, residual, weight=None, *, bias=None, post_weight=None, post_bi
     if type(pair) is int:
         raise MoeLoraError(pair, "moe_lora_block_norm")
     return pair
+
+
+FEW_TOKENS = 16  # the most that forward_few takes
+
+
+def forward_few(x, W1, W2, A1, B1, A2, B2, adapter_ids, *, router_logits=None, topk=None, topk_ids=None, topk_w=None,
+                W1_scale=None, W2_scale=None, y=None, workspace=None) -> torch.Tensor:
+    """The layer for up to 16 tokens in three launches (moe_lora_forward_few): forward's function with
+    router_logits [T][E] float32 and topk, forward_topk's with topk_ids [T][k] int32 (-1: an empty slot) and
+    topk_w [T][k] float32. With W1_scale [E][2I] and W2_scale [E][h] (float32), W1 and W2 are uint8 E4M3
+    codes as in forward_fp8. debug_status(workspace) of a workspace given here tells of logits that were not
+    finite and of ids out of range."""
+    out = (_compiled or _native()).forward_few(x, W1, W2, A1, B1, A2, B2, adapter_ids, router_logits, topk, topk_ids,
+                                               topk_w, W1_scale, W2_scale, y, workspace)
+    if type(out) is int:
+        raise MoeLoraError(out, "moe_lora_forward_few")
+    return out
 
 
 def forward_fp8(x, router_logits, W1q, W1_scale, W2q, W2_scale, A1, B1, A2, B2, adapter_ids,

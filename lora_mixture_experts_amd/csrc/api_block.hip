@@ -1,5 +1,6 @@
 // C ABI of the operators of the block around the layer: the projection with a batch's adapters
-// (moe_lora_linear_lora) and the norms (moe_lora_block_norm), declared in include/moelora.h. Argument
+// (moe_lora_linear_lora), the norms (moe_lora_block_norm), and the layer for a few tokens
+// (moe_lora_forward_few), declared in include/moelora.h. Argument
 // checks and launches.
 #include <algorithm>
 #include <cmath>
@@ -40,9 +41,122 @@ LoraLayout lora_layout(const moe_lora_linear_lora_dims* d, const LinearPlan& p) 
   return L;
 }
 
+int validate_few(const moe_lora_dims* d, int32_t topk) {
+  if (!d) return MOELORA_ENULL;
+  if (d->T < 0 || d->T > kFewTokens || d->hidden <= 0 || d->hidden % 128 != 0 || d->inter <= 0 || d->inter % 128 != 0)
+    return MOELORA_EINVAL_DIMS;
+  if (d->n_experts < 1 || d->n_experts > kMaxExperts || d->n_adapters < 1 || d->n_adapters >= (1 << 28))
+    return MOELORA_EINVAL_DIMS;
+  if (d->rank != 8 && d->rank != 16 && d->rank != 32 && d->rank != 64) return MOELORA_EINVAL_DIMS;
+  if (topk < 1 || topk > d->n_experts || topk > kMaxTopk) return MOELORA_EINVAL_DIMS;
+  // 32-bit byte offsets: one expert's W1, one adapter's A1 of an expert, x, the activations
+  const int64_t h = d->hidden, I = d->inter, most = (int64_t)1 << 31;
+  if (4 * I * h >= most || 2 * d->rank * h >= most || 2 * kFewTokens * h >= most ||
+      4 * (int64_t)kFewTokens * kMaxTopk * I >= most)
+    return MOELORA_EINVAL_DIMS;
+  return MOELORA_OK;
+}
+
+// 16-column tiles a workgroup of the first product takes: as many as leave two workgroups for each of the
+// 256 CUs (fewer parts of z2 to add then), one where even that does not.
+int few_col_tiles(const moe_lora_dims* d, int32_t topk) {
+  const int64_t experts = std::min((int64_t)d->T * topk, (int64_t)d->n_experts);
+  for (int ct = 4; ct > 1; ct /= 2)
+    if (experts * (d->inter / (16 * ct)) >= 512) return ct;
+  return 1;
+}
+
+struct FewLayout {
+  size_t ids, w, pair_flags, lead, z1, act, zpart, total;
+};
+
+FewLayout few_layout(const moe_lora_dims* d, int32_t topk) {
+  const size_t P = (size_t)d->T * (size_t)topk, r = (size_t)d->rank, I = (size_t)d->inter;
+  FewLayout L;
+  size_t at = 256;  // flags first
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align256(bytes);
+    return o;
+  };
+  L.ids = take(4 * P);
+  L.w = take(4 * P);
+  L.pair_flags = take(4 * P);
+  L.lead = take(4 * P);
+  L.z1 = take(4 * P * r);
+  L.act = take(4 * P * I);
+  L.zpart = take(4 * P * r * (I / (16 * (size_t)few_col_tiles(d, topk))));
+  L.total = at;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_lora_few_workspace_size(const moe_lora_dims* d, int32_t topk) {
+  return validate_few(d, topk) == MOELORA_OK ? few_layout(d, topk).total : 0;
+}
+
+int moe_lora_forward_few(const void* x, const float* router_logits, const int32_t* topk_ids,
+                         const float* topk_w, const void* W1, const float* W1_scale, const void* W2,
+                         const float* W2_scale, const void* A1, const void* B1, const void* A2,
+                         const void* B2, const int32_t* adapter_ids, int32_t topk,
+                         const moe_lora_dims* d, void* y, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  int rc = validate_few(d, topk);
+  if (rc != MOELORA_OK || d->T == 0) return rc;
+  const void* big[] = {x, W1, W2, A1, B1, A2, B2, y};
+  for (const void* p : big)
+    if (!p) return MOELORA_ENULL;
+  if (!adapter_ids || !workspace) return MOELORA_ENULL;
+  if (router_logits ? topk_ids || topk_w : false) return MOELORA_EUNSUPPORTED;
+  if (!router_logits && (!topk_ids || !topk_w)) return MOELORA_ENULL;
+  if ((W1_scale != nullptr) != (W2_scale != nullptr)) return MOELORA_ENULL;
+  for (const void* p : big)
+    if (!aligned16(p)) return MOELORA_EALIGN;
+  const void* words[] = {router_logits, topk_ids, topk_w, W1_scale, W2_scale, adapter_ids};
+  for (const void* p : words)
+    if (((uintptr_t)p & 3u) != 0) return MOELORA_EALIGN;
+  const FewLayout L = few_layout(d, topk);
+  if (((uintptr_t)workspace & 255u) != 0 || workspace_bytes < L.total) return MOELORA_EWORKSPACE;
+  rc = check_device();
+  if (rc != MOELORA_OK) return rc;
+  char* const ws = (char*)workspace;
+  const int ct = few_col_tiles(d, topk);
+  FewArgs a;
+  a.x = (const uint16_t*)x;
+  a.logits = router_logits;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.W1 = W1;
+  a.W2 = W2;
+  a.s1 = W1_scale;
+  a.s2 = W2_scale;
+  a.A1 = (const uint16_t*)A1;
+  a.B1 = (const uint16_t*)B1;
+  a.A2 = (const uint16_t*)A2;
+  a.B2 = (const uint16_t*)B2;
+  a.adapter_ids = adapter_ids;
+  a.T = d->T;
+  a.k = topk;
+  a.E = d->n_experts;
+  a.nA = d->n_adapters;
+  a.r = d->rank;
+  a.h = d->hidden;
+  a.I = d->inter;
+  a.tiles = d->inter / (16 * ct);
+  a.y = (uint16_t*)y;
+  a.flags = (int*)ws;
+  a.ids = (int*)(ws + L.ids);
+  a.w = (float*)(ws + L.w);
+  a.pair_flags = (int*)(ws + L.pair_flags);
+  a.lead = (int*)(ws + L.lead);
+  a.z1 = (float*)(ws + L.z1);
+  a.act = (uint16_t*)(ws + L.act);
+  a.zpart = (float*)(ws + L.zpart);
+  return launch_few(a, ct, (hipStream_t)stream) == hipSuccess ? MOELORA_OK : MOELORA_EHIP;
+}
 
 size_t moe_lora_linear_lora_workspace_size(const moe_lora_linear_lora_dims* d) {
   if (validate_linear_lora(d, false) != MOELORA_OK) return 0;

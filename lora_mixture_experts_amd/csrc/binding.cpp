@@ -1,5 +1,5 @@
 // Compiled half of the Python binding for the operators whose kernels take a few microseconds
-// (moe_lora_route, moe_lora_linear, moe_lora_linear_lora, moe_lora_block_norm): checks of torch tensors, outputs and workspaces from torch's
+// (moe_lora_route, moe_lora_linear, moe_lora_linear_lora, moe_lora_block_norm, moe_lora_forward_few): checks of torch tensors, outputs and workspaces from torch's
 // allocator, torch's current stream, one call of the C ABI. As attribute reads and ctypes conversions in
 // Python the same took 6 us of a 10 us call; here 1 us.
 //
@@ -375,10 +375,98 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// forward_few(x, W1, W2, A1, B1, A2, B2, adapter_ids, router_logits, topk, topk_ids, topk_w, W1_scale,
+//             W2_scale, y, workspace) -> y
+PyObject* forward_few(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 16) refuse(PyExc_TypeError, "%s takes 16 arguments%s", "forward_few");
+    const Tensor &x = *tensor_of(a[0], "x"), &W1 = *tensor_of(a[1], "W1"), &A1 = *tensor_of(a[3], "A1");
+    if (x.dim() != 2 || W1.dim() != 3 || A1.dim() != 4)
+      refuse(PyExc_ValueError, "%s must be [T][h], W1 [E][2I][h] and A1 [n_adapters][E][rank][h]%s", "x");
+    const int64_t T = x.size(0), h = x.size(1), E = W1.size(0), I = W1.size(1) / 2, nA = A1.size(0), r = A1.size(2);
+    const int dev = x.is_cuda() ? x.get_device() : -1;
+    const bool w8 = a[12] != Py_None;
+    if (w8 != (a[13] != Py_None)) refuse(PyExc_ValueError, "%s and W2_scale go together%s", "W1_scale");
+    const at::ScalarType wt = w8 ? at::kByte : at::kBFloat16;
+    for (int i = 0; i < 8; ++i) tensor_of(a[i], "each of x, W1, W2, A1, B1, A2, B2 and adapter_ids");
+    const void* px = dense(a[0], "x", at::kBFloat16, {T, h}, dev);
+    const void* pW1 = dense(a[1], "W1", wt, {E, 2 * I, h}, dev);
+    const void* pW2 = dense(a[2], "W2", wt, {E, h, I}, dev);
+    const void* pA1 = dense(a[3], "A1", at::kBFloat16, {nA, E, r, h}, dev);
+    const void* pB1 = dense(a[4], "B1", at::kBFloat16, {nA, E, 2 * I, r}, dev);
+    const void* pA2 = dense(a[5], "A2", at::kBFloat16, {nA, E, r, I}, dev);
+    const void* pB2 = dense(a[6], "B2", at::kBFloat16, {nA, E, h, r}, dev);
+    const void* pids = dense(a[7], "adapter_ids", at::kInt, {T}, dev);
+    const void* ps1 = dense(a[12], "W1_scale", at::kFloat, {E, 2 * I}, dev);
+    const void* ps2 = dense(a[13], "W2_scale", at::kFloat, {E, h}, dev);
+    const bool routes = a[8] != Py_None;
+    if (routes == (a[10] != Py_None) || (a[10] != Py_None) != (a[11] != Py_None))
+      refuse(PyExc_ValueError, "either %s and topk, or topk_ids and topk_w%s", "router_logits");
+    int64_t k;
+    if (routes) {
+      k = PyLong_AsLong(a[9]);
+      if (k == -1 && PyErr_Occurred()) throw Refused{};
+    } else {
+      const Tensor& ids = *tensor_of(a[10], "topk_ids");
+      if (ids.dim() != 2) refuse(PyExc_ValueError, "%s must be a [T][k] tensor%s", "topk_ids");
+      k = ids.size(1);
+      if (a[9] != Py_None) {
+        const long given = PyLong_AsLong(a[9]);
+        if (given == -1 && PyErr_Occurred()) throw Refused{};
+        if (given != k) refuse(PyExc_ValueError, "%s is not the number of topk_ids' columns%s", "topk");
+      }
+    }
+    if (k < INT32_MIN || k > INT32_MAX) refuse(PyExc_ValueError, "%s is too large%s", "topk");
+    const void* logits = dense(a[8], "router_logits", at::kFloat, {T, E}, dev);
+    const void* tids = dense(a[10], "topk_ids", at::kInt, {T, k}, dev);
+    const void* tw = dense(a[11], "topk_w", at::kFloat, {T, k}, dev);
+    moe_lora_dims d;
+    d.T = size32(T, "T");
+    d.hidden = size32(h, "h");
+    d.inter = size32(I, "I");
+    d.n_experts = size32(E, "E");
+    d.n_adapters = size32(nA, "n_adapters");
+    d.rank = size32(r, "rank");
+    const size_t need = moe_lora_few_workspace_size(&d, (int32_t)k);
+    if (!need) return PyLong_FromLong(MOELORA_EINVAL_DIMS);
+    constexpr int inputs[] = {0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 11, 12, 13};
+    Tensor y, ws;
+    if (a[14] == Py_None) {
+      y = at::empty({T, h}, x.options());
+    } else {
+      dense(a[14], "y", at::kBFloat16, {T, h}, dev);
+      y = *tensor_of(a[14], "y");
+      for (const int i : inputs)
+        if (overlap(bytes_of(y), bytes_of(a[i]))) refuse(PyExc_ValueError, "%s overlaps an input%s", "y");
+    }
+    if (a[15] == Py_None) {
+      ws = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
+    } else {
+      ws = *tensor_of(a[15], "workspace");
+      check(ws, "workspace", at::kByte, ws.sizes(), dev);
+      if (!ws.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous%s", "workspace");
+      const Bytes used = dense_bytes(ws.data_ptr(), std::min((int64_t)need, ws.numel()));
+      bool shares = overlap(used, bytes_of(y));
+      for (const int i : inputs) shares |= overlap(used, bytes_of(a[i]));
+      if (shares) refuse(PyExc_ValueError, "%s overlaps another argument%s", "workspace");
+    }
+    const int rc = on_device(dev, [&](void* stream) {
+      return moe_lora_forward_few(px, (const float*)logits, (const int32_t*)tids, (const float*)tw, pW1,
+                                  (const float*)ps1, pW2, (const float*)ps2, pA1, pB1, pA2, pB2,
+                                  (const int32_t*)pids, (int32_t)k, &d, y.data_ptr(), ws.data_ptr(),
+                                  (size_t)ws.numel(), stream);
+    });
+    if (rc != MOELORA_OK) return PyLong_FromLong(rc);
+    if (a[14] != Py_None) return Py_NewRef(a[14]);
+    return THPVariable_Wrap(std::move(y));
+  });
+}
+
 PyMethodDef methods[] = {{"route", (PyCFunction)(void (*)(void))route, METH_FASTCALL, nullptr},
                          {"linear", (PyCFunction)(void (*)(void))linear<false>, METH_FASTCALL, nullptr},
                          {"linear_lora", (PyCFunction)(void (*)(void))linear<true>, METH_FASTCALL, nullptr},
                          {"block_norm", (PyCFunction)(void (*)(void))block_norm, METH_FASTCALL, nullptr},
+                         {"forward_few", (PyCFunction)(void (*)(void))forward_few, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -241,6 +241,31 @@ struct BlockNormArgs {
   float eps, residual_scale, branch_scale;
 };
 
+// The layer for a few tokens (moe_lora_forward_few).
+constexpr int kFewTokens = 16;
+struct FewArgs {
+  const uint16_t* x;       // [T][h]
+  const float* logits;     // [T][E], or nullptr with the choice given:
+  const int* topk_ids;     // [T][k]
+  const float* topk_w;     // [T][k]
+  const void *W1, *W2;     // bf16, or E4M3 codes with the scales s1, s2
+  const float *s1, *s2;    // [E][2I], [E][h], or nullptr
+  const uint16_t *A1, *B1, *A2, *B2;
+  const int* adapter_ids;  // [T]
+  int T, k, E, nA, r, h, I;
+  int tiles;  // column tiles of the first product
+  uint16_t* y;  // [T][h]
+  // workspace; P = T k pairs t * k + j
+  int* flags;       // [1]
+  int* ids;         // [P] expert, -1 for an empty slot
+  float* w;         // [P]
+  int* pair_flags;  // [P]
+  int* lead;        // [P]: 1 for the first pair that names its expert
+  float* z1;        // [P][r]
+  uint16_t* act;    // [P][2][I]: high and low parts
+  float* zpart;     // [P][tiles][r]: z2 of each column tile
+};
+
 // Tile shape of the LDS-staged GEMM: nw wavefronts of WM x WN each; NST LDS stages of BK k.
 struct TiledConfig {
   int bm, bn, wm, wn;
@@ -280,6 +305,7 @@ hipError_t launch_tiled(const TiledConfig& c, bool gateup, const GemmArgs& a, hi
 hipError_t launch_linear_stream(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t stream);
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+hipError_t launch_few(const FewArgs& a, int col_tiles, hipStream_t stream);
 hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream);
 hipError_t launch_linear_lora(const LinearPlan& p, const LinearArgs& a, hipStream_t stream);
 hipError_t launch_sgmv_expand(const SgmvArgs& a, int max_blocks, hipStream_t stream);

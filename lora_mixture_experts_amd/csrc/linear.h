@@ -121,7 +121,11 @@ struct ScaleBias {
 
 // Eight values of a token's z (fp32) as one MFMA operand of the expand z B^T. z keeps some 16 bits: it
 // enters as two bf16, high and low = bf16(z - high), whose columns lie one after the other, so that the
-// reduction is 2 r long and each of B's columns is taken twice.
+// reduction is 2 r long and each of B's columns is taken twice. (Where high is infinite low is 0.)
+__device__ __forceinline__ float low_part(float v, float high) {
+  const float d = v - high;
+  return fabsf(d) < INFINITY ? d : 0.f;
+}
 __device__ __forceinline__ u32x4 z_operand(const float* z, bool low) {
   const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = *reinterpret_cast<const f32x4*>(z + 4);
   uint32_t w[4];
@@ -129,7 +133,7 @@ __device__ __forceinline__ u32x4 z_operand(const float* z, bool low) {
   for (int i = 0; i < 4; ++i) {
     const float lo = i < 2 ? z0[2 * i] : z1[2 * i - 4], hi = i < 2 ? z0[2 * i + 1] : z1[2 * i - 3];
     const uint32_t top = to_bf16x2(lo, hi);
-    w[i] = low ? to_bf16x2(lo - bf16_lo(top), hi - bf16_hi(top)) : top;
+    w[i] = low ? to_bf16x2(low_part(lo, bf16_lo(top)), low_part(hi, bf16_hi(top))) : top;
   }
   return u32x4{w[0], w[1], w[2], w[3]};
 }

@@ -12,12 +12,9 @@
 #include "kernels.h"
 #include "linear_stream.h"
 #include "linear_tiled.h"
+#include "shrink_rows.h"
 
 namespace moelora {
-
-namespace {
-constexpr int kShrinkWaves = 8;
-}
 
 // Shrink. A workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
 // index blockIdx.y, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (no
@@ -63,52 +60,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       xo[nt] = (who >> (nt * 16 + m)) & 1u ? (uint32_t)((nt * 16 + m) * a.ldx * 2) : kOutOfRange;
-    f32x4 acc[NQ][NT];
-#pragma unroll
-    for (int c = 0; c < NQ; ++c)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[c][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    struct Set {
-      u32x4 w[NQ][2], x[NT][2];
-    };
-    auto load = [&](Set& s, int step) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = (step * WK + wk) * 64 + 32 * j + 8 * kq;
-        const bool in = k < K;
-#pragma unroll
-        for (int c = 0; c < NQ; ++c) s.w[c][j] = bufld16(ar, in ? ao[c] + (uint32_t)(k * 2) : kOutOfRange);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s.x[nt][j] = bufld16(xr, in ? xo[nt] + (uint32_t)(k * 2) : kOutOfRange);
-      }
-    };
-    auto compute = [&](const Set& s) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int c = 0; c < NQ; ++c)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[c][nt] = mfma16(s.w[c][j], s.x[nt][j], acc[c][nt]);
-    };
-    const int nsteps = (K + 64 * WK - 1) / (64 * WK);
-    Set sa, sb;
-    load(sa, 0);
-    for (int i = 0; i < nsteps; i += 2) {  // (steps past the end load and add zeros)
-      load(sb, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(sa);
-      __builtin_amdgcn_sched_barrier(0);
-      load(sa, i + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(sb);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __syncthreads();  // (the sums of the adapter before have been read)
-#pragma unroll
-    for (int c = 0; c < NQ; ++c)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) part[wk][c][nt][lane] = acc[c][nt];
-    __syncthreads();
+    shrink_rows<NQ, NT>(part, ar, ao, xr, xo, K, wk, lane);
     // lane: z columns 16 c + 4 kq .. + 3 of token nt * 16 + m
     for (int i = wk; i < NQ * NT; i += WK) {
       const int c = i / NT, nt = i % NT, q = 16 * c + 4 * kq;
