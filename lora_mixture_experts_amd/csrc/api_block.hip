@@ -31,11 +31,32 @@ struct LoraLayout {
   size_t z, groups, part, total;
 };
 
+// Workgroups of the shrink: `slots` that share the adapters of 32 tokens, `splits` that share K (not below 512
+// of it). Up to 512 tokens may all be of different requests; more are prompts, where most of 32 tokens have
+// one adapter and a third workgroup finds nothing to do. K is split where that leaves CUs idle. Measured (us,
+// K = 4096): 64 tokens of 8 adapters, 8 slots, 1 to 8 splits 9.0 6.2 4.8 4.5; 256 tokens of 64, 32 slots 11.4
+// 10.0 15.4 26.2, 8 slots 28.2 18.1 12.9 14.2; 1024 tokens in runs, 4 slots 13.3 8.2 5.6 6.8; 4096 in runs, rank
+// 64, 4 slots 24.3 26.8 25.7 41.3, 32 slots 33.6 53.0.
+struct ShrinkPlan {
+  int slots, splits;
+};
+
+ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
+  const int T = d->linear.T, groups = std::max(1, (T + 31) / 32);
+  ShrinkPlan p;
+  p.slots = std::max(1, std::min({T <= 512 ? 32 : 4, T, d->n_adapters}));
+  const int busy = groups * (T <= 512 ? p.slots : 1);
+  p.splits = 1;
+  const int few = T <= 512 ? 257 : 128;  // busy workgroups
+  while (p.splits < 8 && busy * p.splits < few && d->linear.in_features >= 1024 * p.splits) p.splits *= 2;
+  return p;
+}
+
 LoraLayout lora_layout(const moe_lora_linear_lora_dims* d, const LinearPlan& p) {
   const size_t T = (size_t)d->linear.T;
   LoraLayout L;
   L.z = 256;
-  L.groups = L.z + align256(sizeof(float) * T * (size_t)d->rank);
+  L.groups = L.z + align256(sizeof(float) * T * (size_t)d->rank * (size_t)plan_shrink(d).splits);
   L.part = L.groups + align256(sizeof(TokenAdapters) * ((T + 31) / 32));
   L.total = L.part + linear_workspace(&d->linear, p);
   return L;
@@ -66,6 +87,13 @@ int few_col_tiles(const moe_lora_dims* d, int32_t topk) {
   return 1;
 }
 
+// Workgroups that share a pair's z1: up to four for some 64 pairs, not below 512 of K each.
+int few_z_splits(const moe_lora_dims* d, int32_t topk) {
+  int s = 1;
+  while (s < 4 && d->T * topk * s <= 64 && d->hidden >= 1024 * s) s *= 2;
+  return s;
+}
+
 struct FewLayout {
   size_t ids, w, pair_flags, lead, z1, act, zpart, total;
 };
@@ -83,7 +111,7 @@ FewLayout few_layout(const moe_lora_dims* d, int32_t topk) {
   L.w = take(4 * P);
   L.pair_flags = take(4 * P);
   L.lead = take(4 * P);
-  L.z1 = take(4 * P * r);
+  L.z1 = take(4 * P * r * (size_t)few_z_splits(d, topk));
   L.act = take(4 * P * I);
   L.zpart = take(4 * P * r * (I / (16 * (size_t)few_col_tiles(d, topk))));
   L.total = at;
@@ -153,6 +181,7 @@ int moe_lora_forward_few(const void* x, const float* router_logits, const int32_
   a.pair_flags = (int*)(ws + L.pair_flags);
   a.lead = (int*)(ws + L.lead);
   a.z1 = (float*)(ws + L.z1);
+  a.z_splits = few_z_splits(d, topk);
   a.act = (uint16_t*)(ws + L.act);
   a.zpart = (float*)(ws + L.zpart);
   return launch_few(a, ct, (hipStream_t)stream) == hipSuccess ? MOELORA_OK : MOELORA_EHIP;
@@ -202,13 +231,14 @@ int moe_lora_linear_lora(const void* x, const void* W, const float* w_scale, con
   sh.r = d->rank;
   sh.z = (float*)(ws + L.z);
   sh.groups = (TokenAdapters*)(ws + L.groups);
-  // about four workgroups a CU, and none that can have no adapter
-  const int groups = (l.T + 31) / 32;
-  sh.slots = std::max(1, std::min({1024 / groups, 32, l.T, d->n_adapters}));
+  const ShrinkPlan sp = plan_shrink(d);
+  sh.slots = sp.slots;
+  sh.splits = sp.splits;
   if (launch_token_shrink(sh, stream) != hipSuccess) return MOELORA_EHIP;
 
   LinearArgs a = linear_args(x, W, w_scale, bias, residual, &l, y, ws + L.part);
   a.z = sh.z;
+  a.z_splits = sp.splits;
   a.B = (const uint16_t*)B;
   a.groups = sh.groups;
   a.flags = (int*)ws;

@@ -185,9 +185,10 @@ struct TokenShrinkArgs {
   const int* adapter_ids;  // [T]
   int64_t ldx;
   int T, K, nA, r;
-  float* z;  // [T][r], rows without an adapter unwritten
+  float* z;  // [splits][T][r]: sums of each split of K, rows without an adapter unwritten
   TokenAdapters* groups;  // [ceil(T / 32)]
-  int slots;  // workgroups that share the adapters of 32 tokens
+  int slots;   // workgroups that share the adapters of 32 tokens
+  int splits;  // workgroups that share K: 1, 2, 4 or 8
 };
 
 // Dense projection y = act(scale * (x W^T) + bias) + residual (moe_lora_linear), with adapters
@@ -212,7 +213,8 @@ struct LinearArgs {
   float* part;  // [splits][T][rows] sums of the K splits (splits > 1)
   int splits, row_tiles, col_tiles;
   // with adapters
-  const float* z;               // [T][r]
+  const float* z;               // [z_splits][T][r], added in this order
+  int z_splits;
   const uint16_t* B;            // [nA][rows][r]
   const TokenAdapters* groups;  // [ceil(T / 32)]
   int* flags;                   // [1]: the workspace's
@@ -261,7 +263,8 @@ struct FewArgs {
   float* w;         // [P]
   int* pair_flags;  // [P]
   int* lead;        // [P]: 1 for the first pair that names its expert
-  float* z1;        // [P][r]
+  float* z1;        // [z_splits][P][r], added in this order
+  int z_splits;
   uint16_t* act;    // [P][2][I]: high and low parts
   float* zpart;     // [P][tiles][r]: z2 of each column tile
 };

@@ -119,23 +119,48 @@ struct ScaleBias {
   }
 };
 
-// Eight values of a token's z (fp32) as one MFMA operand of the expand z B^T. z keeps some 16 bits: it
-// enters as two bf16, high and low = bf16(z - high), whose columns lie one after the other, so that the
-// reduction is 2 r long and each of B's columns is taken twice. (Where high is infinite low is 0.)
+// z of a token enters the expand z B^T with some 16 bits: as two bf16, high and low = bf16(z - high), whose
+// columns lie one after the other, so that the reduction is 2 r long and each of B's columns is taken twice.
+// (Where high is infinite low is 0.)
 __device__ __forceinline__ float low_part(float v, float high) {
   const float d = v - high;
   return fabsf(d) < INFINITY ? d : 0.f;
 }
-__device__ __forceinline__ u32x4 z_operand(const float* z, bool low) {
-  const f32x4 z0 = *reinterpret_cast<const f32x4*>(z), z1 = *reinterpret_cast<const f32x4*>(z + 4);
-  uint32_t w[4];
+
+template <int S>
+__device__ __forceinline__ void z_sum(float (&v)[8], const float* z, int64_t split) {
+  f32x4 p[S][2];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p[s][i] = *reinterpret_cast<const f32x4*>(z + s * split + 4 * i);
+#pragma unroll
+  for (int s = 1; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p[0][i] += p[s][i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = p[0][i / 4][i % 4];
+}
+
+// z of token t, ranks q .. q + 7, as high and low operands (zeros for a token past the end).
+__device__ __forceinline__ void z_operands(const LinearArgs& a, int t, int q, u32x4& high, u32x4& low) {
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (t < a.T) {
+    const float* z = a.z + (int64_t)t * a.r + q;
+    const int64_t split = (int64_t)a.T * a.r;
+    if (a.z_splits == 1) z_sum<1>(v, z, split);
+    else if (a.z_splits == 2) z_sum<2>(v, z, split);
+    else if (a.z_splits == 4) z_sum<4>(v, z, split);
+    else z_sum<8>(v, z, split);
+  }
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = i < 2 ? z0[2 * i] : z1[2 * i - 4], hi = i < 2 ? z0[2 * i + 1] : z1[2 * i - 3];
-    const uint32_t top = to_bf16x2(lo, hi);
-    w[i] = low ? to_bf16x2(low_part(lo, bf16_lo(top)), low_part(hi, bf16_hi(top))) : top;
+    h[i] = to_bf16x2(v[2 * i], v[2 * i + 1]);
+    l[i] = to_bf16x2(low_part(v[2 * i], bf16_lo(h[i])), low_part(v[2 * i + 1], bf16_hi(h[i])));
   }
-  return u32x4{w[0], w[1], w[2], w[3]};
+  high = u32x4{h[0], h[1], h[2], h[3]};
+  low = u32x4{l[0], l[1], l[2], l[3]};
 }
 
 // The flag of moe_lora_debug_status for a call with adapters: one wavefront, once every group is written.

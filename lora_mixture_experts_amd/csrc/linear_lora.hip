@@ -17,7 +17,7 @@
 namespace moelora {
 
 // Shrink. A workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
-// index blockIdx.y, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (no
+// index `slot`, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (no
 // sort by adapter: the tokens of a prompt lie together anyway, and those of a decode batch are mostly of
 // different requests). 16x16x32 MFMAs with the rows of A on their A side and 16 tokens on their B side;
 // tokens without the adapter load zeros, which costs no traffic, and their sums are dropped. The eight
@@ -30,14 +30,30 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
   const int lane = threadIdx.x & 63;
   const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kq = lane >> 4;
-  const int t0 = blockIdx.x * 32, K = a.K, r = a.r;
+  // Workgroup ids go round-robin over the 8 XCDs. From 8 groups on each takes consecutive groups: those of one
+  // prompt read its adapter's A through one L2.
+  const int groups = (a.T + 31) / 32, slot = blockIdx.y;
+  int group, sp;
+  if (groups < 8) {
+    group = blockIdx.x / a.splits;
+    sp = blockIdx.x - group * a.splits;
+  } else {
+    const int per = (groups + 7) >> 3, i = blockIdx.x >> 3;
+    group = (blockIdx.x & 7) * per + i / a.splits;
+    sp = i % a.splits;
+    if (i / a.splits >= per || group >= groups) return;
+  }
+  const int t0 = group * 32, K = a.K, r = a.r;
 
   // the group's adapters, found by every wavefront for itself
   const int given = lane < 32 && t0 + lane < a.T ? a.adapter_ids[t0 + lane] : -1;
   const int ad = sanitize_adapter(given, a.nA);
   const bool bad = __ballot(given != ad && given != -1) != 0;
-  TokenAdapters* const grp = a.groups + blockIdx.x;
-  const bool writes = blockIdx.y == 0 && wk == 0;
+  TokenAdapters* const grp = a.groups + group;
+  const bool writes = slot == 0 && sp == 0 && wk == 0;
+  // this split's K range, in whole 64-wide chunks
+  const int chunks = (K + 63) / 64;
+  const int k0 = chunks * sp / a.splits * 64, k1 = min(K, chunks * (sp + 1) / a.splits * 64);
 
   __shared__ f32x4 part[WK][NQ][NT][64];
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X + (int64_t)t0 * a.ldx, 0x7fffffffu);
@@ -52,7 +68,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
       grp->adapter[index] = one;
       grp->tokens[index] = who;
     }
-    if (index % a.slots != (int)blockIdx.y) continue;
+    if (index % a.slots != slot) continue;
     const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.A + (int64_t)one * r * K, (uint32_t)((size_t)r * K * 2));
     uint32_t ao[NQ], xo[NT];
 #pragma unroll
@@ -60,7 +76,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       xo[nt] = (who >> (nt * 16 + m)) & 1u ? (uint32_t)((nt * 16 + m) * a.ldx * 2) : kOutOfRange;
-    shrink_rows<NQ, NT>(part, ar, ao, xr, xo, K, wk, lane);
+    shrink_rows<NQ, NT>(part, ar, ao, xr, xo, k0, k1, wk, lane);
     // lane: z columns 16 c + 4 kq .. + 3 of token nt * 16 + m
     for (int i = wk; i < NQ * NT; i += WK) {
       const int c = i / NT, nt = i % NT, q = 16 * c + 4 * kq;
@@ -68,7 +84,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 #pragma unroll
       for (int p = 1; p < WK; ++p) sum += part[p][c][nt][lane];
       if (q < r && ((who >> (nt * 16 + m)) & 1u))
-        *reinterpret_cast<f32x4*>(a.z + ((int64_t)t0 + nt * 16 + m) * r + q) = sum;
+        *reinterpret_cast<f32x4*>(a.z + ((int64_t)sp * a.T + t0 + nt * 16 + m) * r + q) = sum;
     }
   }
   if (writes && lane == 0) {
@@ -79,8 +95,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 
 hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream) {
   if (a.T <= 0) return hipSuccess;
-  if (a.slots < 1 || a.slots > 32 || a.K % 8 != 0) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((a.T + 31) / 32), (unsigned)a.slots), block(64 * kShrinkWaves);
+  if (a.slots < 1 || a.slots > 32 || a.splits < 1 || a.splits > 8 || a.K % 8 != 0) return hipErrorInvalidValue;
+  const int groups = (a.T + 31) / 32;
+  const dim3 grid((unsigned)((groups < 8 ? groups : (groups + 7) / 8 * 8) * a.splits), (unsigned)a.slots);
+  const dim3 block(64 * kShrinkWaves);
   const bool one = a.T <= 16;
 #define MOELORA_TOKEN_SHRINK(NQ_)                                                              \
   if (one) hipLaunchKernelGGL((token_shrink_kernel<NQ_, 1>), grid, block, 0, stream, a);       \

@@ -116,28 +116,14 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
   const int nsteps = (K + 64 * WK - 1) / (64 * WK);
   Set sa, sb;
   load(sa, 0);
-  for (int i = 0; i < nsteps; i += 2) {
-    // (the barriers keep the compiler from mixing the phases, which would bring the waits for the
-    // set in flight in front of the MFMAs; steps past the end load and add zeros)
-    load(sb, i + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(sa);
-    __builtin_amdgcn_sched_barrier(0);
-    load(sa, i + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(sb);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-
+  // the adapters' term, behind the first weight loads so that its own chain of loads (adapters, z, B) runs
+  // beside them
+  [[maybe_unused]] f32x4 lora[NH][NT];
   if constexpr (LORA) {
-    if (W8) {
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[h][nt][c] *= add[h].s[c];
-    }
+      for (int nt = 0; nt < NT; ++nt) lora[h][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int r = a.r;
     int taken = 0;  // items of the groups before
 #pragma unroll
@@ -163,8 +149,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
             bv[h] = in && n0 + m < a.N ? ldg16(Ba + ((int64_t)h * a.N + n0 + m) * r + rank) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int tok = 32 * g + 16 * q + m;
-            zv[q] = in && tok < a.T ? z_operand(a.z + (int64_t)tok * r + rank, low) : u32x4{0u, 0u, 0u, 0u};
+            u32x4 zh, zl;
+            z_operands(a, in ? 32 * g + 16 * q + m : a.T, rank, zh, zl);
+            zv[q] = low ? zl : zh;
           }
 #pragma unroll
           for (int h = 0; h < NH; ++h)
@@ -178,11 +165,32 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 #pragma unroll
           for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[h][2 * g + q < NT ? 2 * g + q : 0][c] += mine ? term[h][q][c] : 0.f;
+            for (int c = 0; c < 4; ++c) lora[h][2 * g + q < NT ? 2 * g + q : 0][c] += mine ? term[h][q][c] : 0.f;
         }
       }
       taken += items;
     }
+  }
+  for (int i = 0; i < nsteps; i += 2) {
+    // (the barriers keep the compiler from mixing the phases, which would bring the waits for the
+    // set in flight in front of the MFMAs; steps past the end load and add zeros)
+    load(sb, i + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(sa);
+    __builtin_amdgcn_sched_barrier(0);
+    load(sa, i + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(sb);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  if constexpr (LORA) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[h][nt][c] = (W8 ? acc[h][nt][c] * add[h].s[c] : acc[h][nt][c]) + lora[h][nt][c];
     if (blockIdx.x == 0 && wk == WK - 1) report_adapter_range(a);
   }
 

@@ -54,36 +54,267 @@ struct LinearLoader {
   }
 };
 
-// Adapter term of 32 token rows of a wavefront's accumulators: for each adapter among them (those of
-// index part, part + parts, ..), rows wrow[j] of B_a by z of the 32 tokens, straight from global memory
-// into registers (B's columns of an adapter are 32 x r per fragment, one to four 16-byte loads a lane),
-// as a product of its own, of which only the tokens that carry the adapter take their sums: an adapter's
-// infinities and NaNs stay with its tokens. wrow: the lane's weight row, -1 past the end.
+// acc += term where the token of a register carries the adapter (who: the 32 tokens of the fragment).
+__device__ __forceinline__ void add_term(f32x16& acc, const f32x16& term, uint32_t who, int fg) {
+  const uint32_t mine = who >> (4 * fg);  // bit 8 (v / 4) + v % 4: the token of register v
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] += (mine >> (8 * (v / 4) + v % 4)) & 1u ? term[v] : 0.f;
+}
+
+// The largest magnitudes of the two halves' bf16 so far; 0x7f80 and above: infinity or NaN.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void largest(u16x2& m, u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 x = __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu);
+    m = u16x2{m[0] > x[0] ? m[0] : x[0], m[1] > x[1] ? m[1] : x[1]};
+  }
+}
+__device__ __forceinline__ bool all_finite(u16x2 m) { return __ballot(m[0] >= 0x7f80 || m[1] >= 0x7f80) == 0; }
+
+// Adapters' terms of the 32 token rows of a wavefront with one row of FN fragments: for each adapter among them
+// (those of index part, part + parts, ..), rows wrow[j] of B_a by z of the tokens that carry it, zeros for the
+// others. Where B has infinities or NaNs, zeros would not keep them off the others: then the product is one of
+// its own, added to the tokens that carry the adapter (as every adapter's, that took 4 us more of 256 tokens of 64
+// adapters, 4096 x 4096: 64 selects for two products).
+// B comes straight from global memory into registers, eight operands at a time, and the first eight are
+// loaded while the main loop's first tiles are on their way: one adapter after another behind the main loop
+// took 256 tokens of 64 adapters, 4096 x 4096, 36.8 us; 16 operands in flight 25.0.
+// NB: operands of 16 ranks in a row of B (rank 8 and 16: 1, 32: 2, 64: 4). wrow: the lane's row of B, -1 past the
+// end.
 template <int FN>
-__device__ __forceinline__ void add_adapters32(f32x16 (&acc)[FN], const LinearArgs& a, int t0, const int64_t (&wrow)[FN],
-                                               int part, int parts, int lane) {
-  const int fr = lane & 31, fg = lane >> 5, r = a.r;
-  const TokenAdapters& grp = a.groups[t0 >> 5];
-  const int items = grp.n, tok = t0 + fr;
-  for (int i = part; i < items; i += parts) {
-    const uint16_t* Ba = a.B + (int64_t)grp.adapter[i] * a.rows * r;
-    const uint32_t who = grp.tokens[i] >> (4 * fg);  // bit 8 (v / 4) + v % 4: the token of register v
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      f32x16 term;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) term[v] = 0.f;
-      for (int c = 0; c < 2 * r; c += 16) {
-        const int kk = c + 8 * fg;
-        const bool low = kk >= r;
-        const int rank = low ? kk - r : kk;
-        const u32x4 zv = tok < a.T ? z_operand(a.z + (int64_t)tok * r + rank, low) : u32x4{0u, 0u, 0u, 0u};
-        const u32x4 bv = wrow[j] >= 0 ? ldg16(Ba + wrow[j] * r + rank) : u32x4{0u, 0u, 0u, 0u};
-        term = mfma32(zv, bv, term);
+struct AdapterRows {
+  static constexpr int kOperands = 8;
+  int n, adapter;  // adapters of the 32 tokens, one a lane
+  uint32_t tokens;
+  uint32_t bo[FN];
+  u32x4 z[8], b[kOperands];
+
+  __device__ __forceinline__ void load(const LinearArgs& a, int t0, const int64_t (&wrow)[FN], int lane) {
+    n = 0;
+    adapter = -1;
+    tokens = 0u;
+    if (t0 < a.T) {
+      const TokenAdapters& g = a.groups[t0 >> 5];
+      n = g.n;
+      if (lane < 32) {  // (entries from n on are not read below)
+        adapter = g.adapter[lane];
+        tokens = g.tokens[lane];
       }
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[j][v] += (who >> (8 * (v / 4) + v % 4)) & 1u ? term[v] : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      bo[j] = wrow[j] >= 0 ? (uint32_t)((wrow[j] * a.r + (a.r == 8 ? 0 : 8 * (lane >> 5))) * 2) : kOutOfRange;
+  }
+  template <int NB>
+  __device__ __forceinline__ void load_b(const LinearArgs& a, int i, int parts) {
+    constexpr int D = kOperands / (FN * NB);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int one = __builtin_amdgcn_readlane(adapter, min(i + d * parts, n - 1));
+      const __amdgpu_buffer_rsrc_t br = make_rsrc(a.B + (int64_t)one * a.rows * a.r, 0x7fffffffu);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int c = 0; c < NB; ++c) b[(d * FN + j) * NB + c] = bufld16(br, bo[j] + 32u * c);
+    }
+  }
+  template <int NB>
+  __device__ __forceinline__ void load_first(const LinearArgs& a, int t0, int part, int parts, int lane) {
+    if (part >= n) return;
+    const int fg = lane >> 5;
+    // (rank 8: the two halves of the wavefront hold high and low of the same ranks)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+      z_operands(a, t0 + (lane & 31), a.r == 8 ? 0 : 16 * c + 8 * fg, z[2 * c], z[2 * c + 1]);
+      if (a.r == 8) {
+        if (fg) z[2 * c] = z[2 * c + 1];
+        z[2 * c + 1] = u32x4{0u, 0u, 0u, 0u};
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (one operand's parts in registers at a time)
+    }
+    load_b<NB>(a, part, parts);
+  }
+  __device__ __forceinline__ void load_first(const LinearArgs& a, int t0, int part, int parts, int lane) {
+    if (a.r <= 16) load_first<1>(a, t0, part, parts, lane);
+    else if (a.r == 32) load_first<2>(a, t0, part, parts, lane);
+    else load_first<4>(a, t0, part, parts, lane);
+  }
+  template <int NB>
+  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int part, int parts, int lane) {
+    constexpr int D = kOperands / (FN * NB);
+    for (int i = part; i < n; i += D * parts) {
+      if (i != part) load_b<NB>(a, i, parts);
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (i + d * parts >= n) break;
+        const uint32_t who = (uint32_t)__builtin_amdgcn_readlane((int)tokens, i + d * parts);
+        u16x2 most = {0, 0};
+#pragma unroll
+        for (int j = 0; j < FN * NB; ++j) largest(most, b[d * FN * NB + j]);
+        if (all_finite(most) || who == 0xffffffffu) {
+          const bool mine = (who >> (lane & 31)) & 1u;
+#pragma unroll
+          for (int c = 0; c < 2 * NB; ++c) {
+            const u32x4 zc = mine ? z[c] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[j] = mfma32(zc, b[(d * FN + j) * NB + c / 2], acc[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            f32x16 term;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) term[v] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2 * NB; ++c) term = mfma32(z[c], b[(d * FN + j) * NB + c / 2], term);
+            add_term(acc[j], term, who, lane >> 5);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int part, int parts, int lane) {
+    if (a.r <= 16) add<1>(acc, a, part, parts, lane);
+    else if (a.r == 32) add<2>(acc, a, part, parts, lane);
+    else add<4>(acc, a, part, parts, lane);
+  }
+};
+
+// The same for a workgroup whose wavefronts' accumulators (FM x FN fragments) leave no registers for it, through
+// LDS once the main loop is done: z of the tile's rows as operands, and the rows of B of one adapter of the tile
+// after another, straight into one of two buffers while the adapter before is multiplied. 16-byte chunks,
+// XOR-swizzled by the row so that fragment reads are free of bank conflicts. (With B in registers as above the
+// accumulators spilled: 4096 x 28672 x 4096, rank 64, 1.60 ms.) wrow_of(i): B's row of row i of the weight tile,
+// -1 past the end. Every wavefront of the workgroup calls it.
+template <int BM, int BN, int NWV, int FM, int FN, class Row>
+__device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const LinearArgs& a, int row0, int wrow0, int wcol0,
+                                                  Row wrow_of, uint16_t* lds, int part, int parts, int wave, int lane) {
+  static_assert(BM == 256 && BN % 256 == 0, "four groups of 32 tokens in two halves of a wavefront");
+  constexpr int NG = BM / 64;  // registers that hold the adapters of the tile's BM / 32 groups, 32 lanes each
+  const int fr = lane & 31, fg = lane >> 5, r = a.r;
+  const int zc = r / 4, zper = 16 / zc;  // chunks of a row of z, rows in 256 bytes
+  const int bc = r / 8, bper = 16 / bc;  // of B
+  auto z_at = [&](int row, int c) { return lds + (row * zc + (c ^ ((row / zper) & (zc - 1)))) * 8; };
+  auto b_chunk = [&](int row, int c) { return row * bc + (c ^ ((row / bper) & (bc - 1))); };
+  uint16_t* const b_lds = lds + BM * zc * 8;  // two buffers of BN * bc chunks
+  int adapter[NG];
+  uint32_t tokens[NG];
+  uint64_t left[NG];
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int t = row0 + 64 * i + 32 * fg;
+    adapter[i] = -1;
+    tokens[i] = 0u;
+    bool in = false;
+    if (t < a.T) {
+      const TokenAdapters& g = a.groups[t >> 5];
+      in = fr < g.n;
+      adapter[i] = g.adapter[fr];
+      tokens[i] = g.tokens[fr];
+    }
+    left[i] = __ballot(in);
+  }
+  uint32_t who[FM];  // tokens of this wavefront's fragments that carry the adapter
+  int turn = 0;
+  auto next = [&](uint32_t (&w)[FM]) {  // the next adapter of this part, -1 at the end
+    while (true) {
+      int one = -1;
+#pragma unroll
+      for (int i = NG - 1; i >= 0; --i)
+        if (left[i]) one = __builtin_amdgcn_readlane(adapter[i], __builtin_ctzll(left[i]));
+      if (one < 0) return -1;
+#pragma unroll
+      for (int f = 0; f < FM; ++f) w[f] = 0u;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint64_t hit = __ballot(adapter[i] == one) & left[i];
+        left[i] &= ~hit;
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+          const int g = wrow0 / 32 + f;  // its group among the tile's
+          const uint32_t mine = g / 2 == i ? (uint32_t)(hit >> (32 * (g & 1))) : 0u;
+          if (mine) w[f] = (uint32_t)__builtin_amdgcn_readlane((int)tokens[i], 32 * (g & 1) + __builtin_ctz(mine));
+        }
+      }
+      if (turn++ % parts == part) return one;
+    }
+  };
+  const int blocks = BN * bc / 64;  // of 64 chunks, one a lane
+  auto load = [&](int one, int buf) {
+    const u32x4 br = buffer_desc(a.B + (int64_t)one * a.rows * r, 0x7fffffffu);
+    for (int i = wave; i < blocks; i += NWV) {
+      const int at = i * 64 + lane, row = at / bc, c = (at - row * bc) ^ ((row / bper) & (bc - 1));
+      const int64_t w = wrow_of(row);
+      lds_dma16(br, w >= 0 ? (uint32_t)((w * r + 8 * c) * 2) : kOutOfRange, 0u,
+                (uint32_t)(uintptr_t)(b_lds + (buf * BN * bc + i * 64) * 8));
+    }
+  };
+  int one = next(who);
+  if (one < 0) return;
+  __syncthreads();  // (the stages are free)
+  load(one, 0);
+  for (int i = threadIdx.x; i < BM * bc; i += 64 * NWV) {
+    const int row = i / bc, c = i - row * bc;
+    u32x4 high, low;
+    z_operands(a, row0 + row, 8 * c, high, low);
+    *reinterpret_cast<u32x4*>(z_at(row, c)) = high;
+    *reinterpret_cast<u32x4*>(z_at(row, bc + c)) = low;
+  }
+  int buf = 0;
+  while (one >= 0) {
+    wait_vmcnt<0>();
+    __syncthreads();
+    uint32_t now[FM];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) now[f] = who[f];
+    one = next(who);
+    if (one >= 0) load(one, buf ^ 1);
+    const uint16_t* const b0 = b_lds + buf * BN * bc * 8;
+    auto frag = [&](int j, int c) {
+      return *reinterpret_cast<const u32x4*>(b0 + b_chunk(wcol0 + j * 32 + fr, c) * 8);
+    };
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      if (now[f] == 0u) continue;
+      const int row = wrow0 + f * 32 + fr;
+      // operands of z: high and low of 16 ranks (rank 8: the two halves of the wavefront hold high and low of
+      // the same ranks)
+      const int nz = r == 8 ? 1 : r / 8;
+      auto z_frag = [&](int c) {
+        return *reinterpret_cast<const u32x4*>(z_at(row, r == 8 ? fg : (c & 1) * bc + (c & ~1) + fg));
+      };
+      auto b_frag = [&](int j, int c) { return frag(j, r == 8 ? 0 : (c & ~1) + fg); };
+      bool plain = now[f] == 0xffffffffu;
+      if (!plain) {
+        u16x2 most = {0, 0};
+#pragma unroll 1
+        for (int c = 0; c < nz; c += 2)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) largest(most, b_frag(j, c));
+        plain = all_finite(most);
+      }
+      if (plain) {
+        const bool mine = (now[f] >> fr) & 1u;
+#pragma unroll 1
+        for (int c = 0; c < nz; ++c) {
+          const u32x4 z = mine ? z_frag(c) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[f][j] = mfma32(z, b_frag(j, c), acc[f][j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x16 term;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) term[v] = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < nz; ++c) term = mfma32(z_frag(c), b_frag(j, c), term);
+          add_term(acc[f][j], term, now[f], fg);
+        }
+      }
+    }
+    buf ^= 1;
   }
 }
 
@@ -181,6 +412,19 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
   const bool has_res = a.R && !split;
   if (FM == 1 && has_res) load_residual(0);
 
+  // (the adapters of 32 tokens are dealt to the splits and K groups, whose sums meet in any case)
+  const int part = sp * KG + kg, parts = a.splits * KG;
+  auto wrow_of = [&](int r) {  // B's row of tile row r
+    return col0 + col_of(r) < a.N ? col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0) : (int64_t)-1;
+  };
+  [[maybe_unused]] AdapterRows<FN> rows_ad;
+  if constexpr (LORA && FM == 1) {
+    int64_t wrow[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) wrow[j] = wrow_of(wn * WN + j * 32 + fr);
+    rows_ad.load(a, row0 + wm * WM, wrow, lane);
+  }
+
   f32x16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -188,28 +432,21 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  Pipe::run_steps(acc, ld, lds + kg * (Pipe::LDS_BYTES / 2), nsteps, wave, lane, [] {});
+  Pipe::run_steps(acc, ld, lds + kg * (Pipe::LDS_BYTES / 2), nsteps, wave, lane, [&] {
+    if constexpr (LORA && FM == 1) rows_ad.load_first(a, row0 + wm * WM, part, parts, lane);
+  });
 
-  if constexpr (LORA) {
-    // (the adapter's term takes no weight scale; the adapters of 32 tokens are dealt to the splits and K
-    // groups, whose sums meet in any case)
-    int64_t wrow[FN];
+  if constexpr (LORA) {  // (the adapters' term takes no weight scale)
+    if (W8) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int r = wn * WN + j * 32 + fr;
-      wrow[j] = col0 + col_of(r) < a.N ? col0 + col_of(r) + (is_up(r) ? (int64_t)a.N : 0) : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if (W8) {
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[i][j][v] *= sc[j];
-      }
-      const int t0 = row0 + wm * WM + i * 32;
-      if (t0 < a.T) add_adapters32<FN>(acc[i], a, t0, wrow, sp * KG + kg, a.splits * KG, lane);
     }
+    if constexpr (FM == 1) rows_ad.add(acc[0], a, part, parts, lane);
+    else add_adapters_tile<BM, BN, NWV, FM, FN>(acc, a, row0, wm * WM, wn * WN, wrow_of, lds, part, parts, wave, lane);
 #pragma unroll
     for (int j = 0; j < FN; ++j) sc[j] = 1.f;
     if (tk == 0 && wave_all == NWV * KG - 1) report_adapter_range(a);
@@ -354,6 +591,7 @@ hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
   constexpr int out = KG * NWV * 32 * WN * 4;  // the epilogue's regions
   constexpr int bytes = ring > out ? ring : out;
   static_assert(bytes <= kLdsBytes, "LDS stages must fit");
+  static_assert(WM == 32 || BM * 256 + 2 * BN * 128 <= bytes, "z and two adapters' rows of B of rank 64 must fit");
   auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, KG, GATED, W8, STREAM, LORA>;
   static bool attr_set[64] = {};
   int dev = 0;
