@@ -95,7 +95,7 @@ int few_z_splits(const moe_lora_dims* d, int32_t topk) {
 }
 
 struct FewLayout {
-  size_t ids, w, pair_flags, lead, z1, act, zpart, total;
+  size_t ids, w, pair_flags, members, member_pair, member_w, z1, act, zpart, total;
 };
 
 FewLayout few_layout(const moe_lora_dims* d, int32_t topk) {
@@ -110,7 +110,9 @@ FewLayout few_layout(const moe_lora_dims* d, int32_t topk) {
   L.ids = take(4 * P);
   L.w = take(4 * P);
   L.pair_flags = take(4 * P);
-  L.lead = take(4 * P);
+  L.members = take(4 * P);
+  L.member_pair = take(4 * P * kFewTokens);
+  L.member_w = take(4 * P * kFewTokens);
   L.z1 = take(4 * P * r * (size_t)few_z_splits(d, topk));
   L.act = take(4 * P * I);
   L.zpart = take(4 * P * r * (I / (16 * (size_t)few_col_tiles(d, topk))));
@@ -179,7 +181,9 @@ int moe_lora_forward_few(const void* x, const float* router_logits, const int32_
   a.ids = (int*)(ws + L.ids);
   a.w = (float*)(ws + L.w);
   a.pair_flags = (int*)(ws + L.pair_flags);
-  a.lead = (int*)(ws + L.lead);
+  a.members = (int*)(ws + L.members);
+  a.member_pair = (int*)(ws + L.member_pair);
+  a.member_w = (float*)(ws + L.member_w);
   a.z1 = (float*)(ws + L.z1);
   a.z_splits = few_z_splits(d, topk);
   a.act = (uint16_t*)(ws + L.act);

@@ -54,45 +54,39 @@ struct FewChoice {
 
 // Slot j of a token's choice from its logits, by one wavefront: k rounds of the largest logit, ties to the lower
 // id, on keys that order as the logits do (logits that are not finite as -infinity; 0: taken or no expert).
-// Weights as the layer's own routing gives them.
+// Weights as the layer's own routing gives them. VPL: logits a lane.
+template <int VPL>
 __device__ __forceinline__ FewChoice few_route(const float* logits, int E, int k, int j) {
-  constexpr int VPL = kMaxExperts / 64;
   const int lane = threadIdx.x & 63;
+  float f[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) f[i] = logits[min(lane + 64 * i, E - 1)];
   uint32_t key[VPL];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    key[i] = 0u;
-    if (64 * i >= E) continue;
-    float f = lane + 64 * i < E ? logits[lane + 64 * i] : 0.f;
-    if (!__builtin_isfinite(f)) {
-      bad = true;
-      f = -INFINITY;
-    }
-    const uint32_t u = __float_as_uint(f + 0.f);  // (-0 as 0)
-    if (lane + 64 * i < E) key[i] = (int32_t)u < 0 ? ~u : u | 0x80000000u;
+    const bool finite = __builtin_isfinite(f[i]);
+    bad |= !finite;
+    const uint32_t u = __float_as_uint(finite ? f[i] + 0.f : -INFINITY);  // (-0 as 0)
+    key[i] = lane + 64 * i < E ? ((int32_t)u < 0 ? ~u : u | 0x80000000u) : 0u;
   }
   FewChoice c;
   c.e = -1;
-  float own = 0.f;
   uint32_t mine = 0u;  // lane i: the key of rank i
+#pragma unroll 1
   for (int round = 0; round < k; ++round) {
-    uint32_t best = 0u;
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = best > key[i] ? best : key[i];
+    const uint32_t top = wave_max(best);
+    int id = 1 << 30;  // the lowest id with it: one a lane, then over the lanes
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == top) id = lane + 64 * i;
+    id = (int)~wave_max(~(uint32_t)id);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (64 * i < E) best = best > key[i] ? best : key[i];
-    const uint32_t top = wave_max(best);
-    int id = -1;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (64 * i >= E || id >= 0) continue;
-      const uint64_t has = __ballot(key[i] == top);
-      if (has) {
-        const int at = __builtin_ctzll(has);
-        id = 64 * i + at;
-        if (lane == at) key[i] = 0u;
-      }
-    }
+      if (lane + 64 * i == id) key[i] = 0u;
     if (lane == round) mine = top;
     if (round == j) c.e = id;
   }
@@ -100,19 +94,16 @@ __device__ __forceinline__ FewChoice few_route(const float* logits, int E, int k
   const float first = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 0));
   const float x = lane < k ? (first == -INFINITY ? 1.f : __expf(v - first)) : 0.f;
   float sum = 0.f;
-  for (int i = 0; i < k; ++i) {
-    const float xi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), i));
-    sum += xi;
-    if (i == j) own = xi;
-  }
-  c.w = own * (1.f / sum);
+#pragma unroll 1
+  for (int i = 0; i < k; ++i) sum += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), i));
+  c.w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)) * (1.f / sum);
   c.flags = __ballot(bad) ? 1 : 0;  // MOELORA_FLAG_NONFINITE_LOGIT
   return c;
 }
 
 // One pair t * k + j (blockIdx.x): expert, weight, and z1 over a split of K (blockIdx.y).
 template <int NQ>
-__global__ __launch_bounds__(64 * kShrinkWaves) void few_shrink_kernel(FewArgs a) {
+__global__ __launch_bounds__(64 * kShrinkWaves, 4) void few_shrink_kernel(FewArgs a) {
   __shared__ f32x4 part[kShrinkWaves][NQ][1][64];
   const int tid = threadIdx.x, lane = tid & 63, wk = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p = blockIdx.x, k = a.k, t = p / k, E = a.E, r = a.r, sp = blockIdx.y;
@@ -120,7 +111,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void few_shrink_kernel(FewArgs a
   const int ad = sanitize_adapter(given, a.nA);
   FewChoice c;
   if (a.logits) {
-    c = few_route(a.logits + (int64_t)t * E, E, k, p - t * k);
+    const float* const row = a.logits + (int64_t)t * E;
+    const int j = p - t * k;
+    c = E <= 64 ? few_route<1>(row, E, k, j) : E <= 128 ? few_route<2>(row, E, k, j)
+        : E <= 256 ? few_route<4>(row, E, k, j) : few_route<kMaxExperts / 64>(row, E, k, j);
   } else {
     c.e = a.topk_ids[p];
     c.flags = c.e < -1 || c.e >= E ? 4 : 0;  // MOELORA_FLAG_EXPERT_RANGE
@@ -154,17 +148,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void few_shrink_kernel(FewArgs a
   }
 }
 
-// sum_q z[q] B[q] of one row of B, r a multiple of 8.
-__device__ __forceinline__ float expand_row(const uint16_t* b, const float* z, int r) {
-  float s = 0.f;
-#pragma unroll 2
-  for (int q = 0; q < r; q += 8) {
-    const u32x4 bv = ldg16(b + q);
-    const f32x4 z0 = *reinterpret_cast<const f32x4*>(z + q), z1 = *reinterpret_cast<const f32x4*>(z + q + 4);
-    s += z0[0] * bf16_lo(bv.x) + z0[1] * bf16_hi(bv.x) + z0[2] * bf16_lo(bv.y) + z0[3] * bf16_hi(bv.y);
-    s += z1[0] * bf16_lo(bv.z) + z1[1] * bf16_hi(bv.z) + z1[2] * bf16_lo(bv.w) + z1[3] * bf16_hi(bv.w);
-  }
-  return s;
+// Eight bf16 by eight floats.
+__device__ __forceinline__ float dot8(u32x4 w, const float* x) {
+  return x[0] * bf16_lo(w.x) + x[1] * bf16_hi(w.x) + x[2] * bf16_lo(w.y) + x[3] * bf16_hi(w.y) + x[4] * bf16_lo(w.z) +
+         x[5] * bf16_hi(w.z) + x[6] * bf16_lo(w.w) + x[7] * bf16_hi(w.w);
 }
 
 // k of a lane's operand j of a 128-wide step. bf16: a load covers 64 contiguous bytes of each row; E4M3: 16
@@ -175,20 +162,24 @@ __device__ __forceinline__ int few_k(int j, int kq) {
 }
 
 // CT: 16-column tiles of a workgroup, each shared by 8 / CT wavefronts that take its 128-wide K steps in
-// turn. What follows the main loop waits for little: the adapters' term z1 B1^T is formed behind the first weight
-// loads and A2's rows are loaded there (both after the main loop took a third of a workgroup's time: 2 of 16
-// experts of 4096 x 11008, one token, 72.7 us).
+// turn. The tokens' rows of x lie in LDS, as much of K as fits at a time (a load instruction costs a CU some 50
+// cycles whatever it brings, and x beside E4M3 weights doubled their number). Everything else that a workgroup
+// needs is loaded at once, behind the first weights: under the load of the others' weights a load takes up to 10
+// us, and one after another (z1, then B1, behind the main loop A2) they held a workgroup for half of its time (2
+// of 16 experts of 4096 x 11008, one token, 72.7 us).
 template <int CT, bool W8>
-__global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs a) {
-  constexpr int KW = kFewWaves / CT, NTH = 64 * kFewWaves, C8 = 2 * CT;
-  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = W8 ? 3 : 2, NI = (CT * 16 * kFewTokens + NTH - 1) / NTH;
-  static_assert(NI <= 2, "items of a thread");
+__global__ __launch_bounds__(64 * kFewWaves, 4) void few_gate_up_kernel(FewArgs a) {
+  constexpr int KW = kFewWaves / CT, NTH = 64 * kFewWaves, C8 = 2 * CT, COLS = 16 * CT;
+  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = W8 ? 4 : 2;
+  constexpr int XB = 32 * 1024, XL = XB / 16 / NTH;  // bytes of x, loads of a thread
   __shared__ int s_ids[kFewTokens * kMaxTopk];
-  // the tokens that chose the expert: token, its first pair with it, adapter, z1
+  // the tokens that chose the expert ("members"): token, its first pair with it, adapter, z1, the adapters' term
   __shared__ int s_tok[kFewTokens], s_pair[kFewTokens], s_ad[kFewTokens];
   __shared__ __attribute__((aligned(16))) float s_z[kFewTokens][64];
+  __shared__ float s_lora[kFewTokens][2][COLS];
   __shared__ f32x4 s_part[kFewWaves][2][64];
-  __shared__ float s_act[kFewTokens][CT * 16];
+  __shared__ float s_act[kFewTokens][COLS];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[XB];  // rows (step, member) of 128, 16-byte chunks swizzled
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave % KW, ct = wave / KW;
   const int m = lane & 15, kq = lane >> 4;
@@ -203,22 +194,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs a) 
     for (int j = k - 1; j >= 0; --j)
       if (s_ids[m * k + j] == e) pair = m * k + j;
   const bool leads = e >= 0 && __ballot(pair >= 0 && pair < p0) == 0;
-  if (blockIdx.x == 0 && tid == 0) a.lead[p0] = leads;
-  if (!leads) return;
-  const uint32_t members = (uint32_t)__ballot(pair >= 0) & 0xffffu;
+  const uint32_t members = leads ? (uint32_t)__ballot(pair >= 0) & 0xffffu : 0u;
   const int M = __builtin_popcount(members);
+  if (blockIdx.x == 0 && tid == 0) a.members[p0] = M;
+  if (!leads) return;
 
   const int n0 = (blockIdx.x * CT + ct) * 16;
   __amdgpu_buffer_rsrc_t wr[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     wr[h] = make_rsrc((const uint8_t*)a.W1 + ((int64_t)e * 2 * I + (int64_t)h * I + n0) * K * WB, 0x7fffffffu);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, 0x7fffffffu);
   const uint32_t wo = (uint32_t)(m * K * WB);
-  const uint32_t xo = pair >= 0 ? (uint32_t)(m * K * 2) : kOutOfRange;
   const int steps = K / 128;
   struct Set {
-    u32x4 w[2][WL], x[4];
+    u32x4 w[2][WL];
   };
   auto load = [&](Set& s, int i) {
     const int step = i * KW + wk;
@@ -228,66 +217,128 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs a) 
 #pragma unroll
       for (int j = 0; j < WL; ++j)
         s.w[h][j] = bufld16(wr[h], in ? wo + (uint32_t)((step * 128 + few_k<W8>(W8 ? 2 * j : j, kq)) * WB) : kOutOfRange);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      s.x[j] = bufld16(xr, in ? xo + (uint32_t)((step * 128 + few_k<W8>(j, kq)) * 2) : kOutOfRange);
-  };
-  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-  auto compute = [&](const Set& s) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        acc[h] = mfma16(W8 ? e4m3x8_to_bf16(s.w[h][j / 2 % WL], j % 2) : s.w[h][j % WL], s.x[j], acc[h]);
   };
   const int n = (steps + KW - 1) / KW;
   Set set[NS];
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) load(set[i], i);
 
-  // members in token order, with their z1
+  // the c-th member's token
+  auto token = [&](int c) {
+    uint32_t left = members;
+    for (int i = 0; i < c; ++i) left &= left - 1u;
+    return left ? __builtin_ctz(left) : 0;
+  };
+  // x of the wavefronts' steps from i0 on (past the end: zeros)
+  const int phase = max(1, min(n, XB / (M * 256 * KW)));  // steps of a wavefront whose x is in LDS at once
+  const int x_items = phase * KW * M * 16;
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, 0x7fffffffu);
+  u32x4 xv[XL];
+  auto load_x = [&](int i0) {
+#pragma unroll
+    for (int q = 0; q < XL; ++q) {
+      const int i = q * NTH + tid, row = i / 16, step = row / M;
+      const int at = (i0 * KW + step) * 128 + 8 * (i % 16);
+      const bool in = i < x_items && at < K;
+      xv[q] = bufld16(xr, in ? (uint32_t)((token(in ? row - step * M : 0) * K + at) * 2) : kOutOfRange);
+    }
+  };
+  auto store_x = [&]() {
+#pragma unroll
+    for (int q = 0; q < XL; ++q) {
+      const int i = q * NTH + tid, row = i / 16;
+      if (i < x_items) *reinterpret_cast<u32x4*>(s_x + row * 256 + ((i % 16) ^ (row & 15)) * 16) = xv[q];
+    }
+  };
+  load_x(0);
+  // z1 (its splits added in order), a thread up to two values
+  float z[2] = {0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = q * NTH + tid, c = i / r;
+    const int of = __shfl(pair, token(min(c, M - 1))), has = __shfl(ad, token(min(c, M - 1)));
+    if (c >= M || has < 0) continue;
+    const float* from = a.z1 + (int64_t)of * r + (i - c * r);
+    float v[4];
+#pragma unroll
+    for (int sp = 0; sp < 4; ++sp) v[sp] = sp < a.z_splits ? from[(int64_t)sp * P * r] : 0.f;
+    z[q] = v[0];
+#pragma unroll
+    for (int sp = 1; sp < 4; ++sp) z[q] += v[sp];
+  }
+  // eight ranks of one row of B1 an item, the items of a row side by side; eight columns of one rank of A2
+  const int r8 = r / 8, b_items = M * 2 * COLS * r8, a_items = M * r * C8;
+  auto load_b1 = [&](int i) {
+    const int c = i / (2 * COLS * r8), h = i / (COLS * r8) & 1, col = i / r8 % COLS;
+    const int has = __shfl(ad, token(min(c, M - 1)));
+    if (i >= b_items || has < 0) return u32x4{0u, 0u, 0u, 0u};
+    return ldg16(a.B1 + ((((int64_t)has * a.E + e) * 2 + h) * I + blockIdx.x * COLS + col) * r + 8 * (i % r8));
+  };
+  auto load_a2 = [&](int i) {
+    const int c = i / (r * C8), q = i / C8 % r;
+    const int has = __shfl(ad, token(min(c, M - 1)));
+    if (i >= a_items || has < 0) return u32x4{0u, 0u, 0u, 0u};
+    return ldg16(a.A2 + (((int64_t)has * a.E + e) * r + q) * I + blockIdx.x * COLS + 8 * (i % C8));
+  };
+  const u32x4 b1[2] = {load_b1(tid), load_b1(NTH + tid)};
+  const u32x4 a2 = load_a2(tid);
+  __builtin_amdgcn_sched_barrier(0);
+  store_x();
   if (wave == 0 && lane < 16 && pair >= 0) {
     const int c = __builtin_popcount(members & ((1u << m) - 1u));
     s_tok[c] = m;
     s_pair[c] = pair;
     s_ad[c] = ad;
+    if (blockIdx.x == 0) {  // for few_down: the member's pair and the sum of its weights
+      float w = 0.f;
+      for (int j = pair - m * k; j < k; ++j)
+        if (s_ids[m * k + j] == e) w += a.w[m * k + j];
+      a.member_pair[p0 * kFewTokens + c] = pair;
+      a.member_w[p0 * kFewTokens + c] = w;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = q * NTH + tid;
+    if (i < M * r) s_z[i / r][i % r] = z[q];
   }
   __syncthreads();
-  for (int i = tid; i < M * r; i += NTH) {
-    const int c = i / r, q = i - c * r;
-    if (s_ad[c] < 0) continue;
-    const float* z = a.z1 + (int64_t)s_pair[c] * r + q;
-    float s = z[0];
-    for (int q2 = 1; q2 < a.z_splits; ++q2) s += z[(int64_t)q2 * P * r];
-    s_z[c][q] = s;
+  for (int q = 0; q * NTH < b_items; ++q) {
+    const int i = q * NTH + tid, c = i / (2 * COLS * r8), h = i / (COLS * r8) & 1, col = i / r8 % COLS;
+    const u32x4 w = q == 0 ? b1[0] : q == 1 ? b1[1] : load_b1(i);
+    float s = i < b_items && s_ad[c] >= 0 ? dot8(w, &s_z[c][8 * (i % r8)]) : 0.f;
+    for (int d = 1; d < r8; d *= 2) s += __shfl_xor(s, d);
+    if (i < b_items && i % r8 == 0) s_lora[c][h][col] = s;
   }
-  __syncthreads();
-  // a thread's items: one column of one member each; (its part of A2) eight columns of one rank of a member
-  float lora[NI][2];
-#pragma unroll
-  for (int it = 0; it < NI; ++it) {
-    const int i = it * NTH + tid, c = i / (CT * 16), col = i % (CT * 16);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) lora[it][h] = 0.f;
-    if (c >= M || s_ad[c] < 0) continue;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      lora[it][h] = expand_row(a.B1 + ((((int64_t)s_ad[c] * a.E + e) * 2 + h) * I + blockIdx.x * CT * 16 + col) * r, s_z[c], r);
-  }
-  auto load_a2 = [&](int i) {
-    const int c = i / (r * C8), q = i / C8 % r;
-    if (c >= M || s_ad[c] < 0) return u32x4{0u, 0u, 0u, 0u};
-    return ldg16(a.A2 + (((int64_t)s_ad[c] * a.E + e) * r + q) * I + blockIdx.x * CT * 16 + 8 * (i % C8));
-  };
-  const u32x4 a2 = load_a2(tid);
   __builtin_amdgcn_sched_barrier(0);
 
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  const int column = min(m, M - 1);  // (a product's columns are the members; columns past them are not read)
+  auto compute = [&](const Set& s, int step) {  // of the steps in LDS (one past them: its weights are zeros)
+    const int row = step * M + column;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int chunk = few_k<W8>(j, kq) / 8;
+      const u32x4 x = *reinterpret_cast<const u32x4*>(s_x + row * 256 + (chunk ^ (row & 15)) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        acc[h] = mfma16(W8 ? e4m3x8_to_bf16(s.w[h][j / 2 % WL], j % 2) : s.w[h][j % WL], x, acc[h]);
+    }
+  };
+  int begin = 0;
   for (int i = 0; i < n; i += NS) {
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
+      if (i + q == begin + phase && i + q < n) {
+        begin = i + q;
+        load_x(begin);
+        __syncthreads();
+        store_x();
+        __syncthreads();
+      }
       load(set[(q + NS - 1) % NS], i + q + NS - 1);
       __builtin_amdgcn_sched_barrier(0);
-      compute(set[q]);
+      compute(set[q], min(i + q - begin, phase - 1) * KW + wk);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -295,19 +346,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs a) 
   for (int h = 0; h < 2; ++h) s_part[wave][h][lane] = acc[h];
   __syncthreads();
 
-#pragma unroll
-  for (int it = 0; it < NI; ++it) {
-    const int i = it * NTH + tid, c = i / (CT * 16), col = i % (CT * 16);
-    if (c >= M) continue;
-    const int ncol = blockIdx.x * CT * 16 + col;
+  for (int i = tid; i < M * COLS; i += NTH) {  // one column of a member
+    const int c = i / COLS, col = i % COLS, ncol = blockIdx.x * COLS + col;
     float v[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float s = 0.f;
 #pragma unroll
-      for (int q = 0; q < KW; ++q) s += s_part[col / 16 * KW + q][h][(col % 16 >> 2) * 16 + s_tok[c]][col & 3];
+      for (int q = 0; q < KW; ++q) s += s_part[col / 16 * KW + q][h][(col % 16 >> 2) * 16 + c][col & 3];
       if (W8) s *= a.s1[(int64_t)e * 2 * I + (int64_t)h * I + ncol];
-      v[h] = s + lora[it][h];
+      v[h] = s + s_lora[c][h][col];
     }
     const float act = swiglu(v[0], v[1]);
     const uint32_t hi = to_bf16x2(act, 0.f) & 0xffffu;
@@ -317,39 +365,43 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_gate_up_kernel(FewArgs a) 
   }
   __syncthreads();
   // these columns' part of z2: the C8 threads of a rank meet
-  for (int i0 = 0; i0 < M * r * C8; i0 += NTH) {
+  for (int i0 = 0; i0 < a_items; i0 += NTH) {
     const int i = i0 + tid, c = i / (r * C8), q = i / C8 % r;
-    float s = 0.f;
-    if (c < M && s_ad[c] >= 0) {
-      const u32x4 av = i0 == 0 ? a2 : load_a2(i);
-      const float* x = &s_act[c][8 * (i % C8)];
-      s = x[0] * bf16_lo(av.x) + x[1] * bf16_hi(av.x) + x[2] * bf16_lo(av.y) + x[3] * bf16_hi(av.y);
-      s += x[4] * bf16_lo(av.z) + x[5] * bf16_hi(av.z) + x[6] * bf16_lo(av.w) + x[7] * bf16_hi(av.w);
-    }
+    const u32x4 av = i0 == 0 ? a2 : load_a2(i);
+    const bool in = i < a_items && s_ad[c] >= 0;
+    float s = in ? dot8(av, &s_act[c][8 * (i % C8)]) : 0.f;
 #pragma unroll
     for (int d = 1; d < C8; d *= 2) s += __shfl_xor(s, d);
-    if (c < M && s_ad[c] >= 0 && i % C8 == 0) a.zpart[((int64_t)s_pair[c] * a.tiles + blockIdx.x) * r + q] = s;
+    if (in && i % C8 == 0) a.zpart[((int64_t)s_pair[c] * a.tiles + blockIdx.x) * r + q] = s;
   }
 }
 
-// FT (16 or 8) features of every token. The wavefronts share the 128-wide K steps of all chosen experts, each a
-// contiguous range of them, and add an expert's sums, weighted, to its tokens' (in LDS, a place for each
-// wavefront) at its last step there. Before, behind their first weight loads, they form the adapters' term pair
-// by pair: z2 from its parts, in tile order, and z2 B2^T.
-// The columns of a product are the high parts of 8 tokens' act and their low parts. An expert of more than 8
-// tokens has two products a step (NA = 2), or with NA = 1 comes twice: where experts mostly have fewer, the
-// second product's loads cost more than its weights, read twice (16 tokens, 8 of 128 experts: see DESIGN).
+// FT features of every token. The wavefronts share the K steps of all chosen experts, each a contiguous range of
+// them, and add an expert's sums, weighted, to its tokens' (in LDS, a place for each wavefront) at its last step
+// there. Before, behind their first weight loads, they form the adapters' term: z2 from its parts, in tile
+// order, and z2 B2^T.
+// FT = 16: a step is 128 of K; the columns of a product are the high parts of 8 tokens' act and their low parts,
+// NA products a step. FT = 8, where 16 would leave CUs without a workgroup: a step is 256 of K, whose halves
+// are rows 0 .. 7 and 8 .. 15 of a product and have columns of their own (high and low parts of 4 tokens), so that
+// a load still brings 1 KB. An expert of more tokens than a step has columns for comes several times.
+// act passes through LDS, a region for each wavefront: as many steps at once as the expert's tokens leave room
+// for, so that act costs as few load instructions as its bytes need (a load costs a CU some 50 cycles whatever it
+// brings; an operand a load, as the weights come, doubled their number: 16 tokens, 8 of 128 experts, 135 us).
 template <int FT, int NA, bool W8>
-__global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a) {
-  constexpr int NW = kFewDownWaves, NTH = 64 * NW, MAXP = kFewTokens * kMaxTopk, C = 8 * NA;
-  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = NA == 1 ? 3 : 2;
-  __shared__ int s_ids[MAXP], s_lead[MAXP], s_expert[MAXP], s_n;  // entries: experts, those of many tokens twice
-  __shared__ uint8_t s_part[MAXP];                                // 0, or 1 for the second entry
+__global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(FewArgs a) {
+  constexpr int NW = kFewDownWaves / NA, NTH = 64 * NW, MAXP = kFewTokens * kMaxTopk;
+  constexpr int SUB = FT == 8 ? 2 : 1, C = FT == 8 ? 4 : 8 * NA;  // 128-wide parts of a step; columns of a step
+  static_assert(FT == 16 || NA == 1, "one product of 4 tokens in 8 features' steps");
+  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = W8 ? 6 : 3, AL = 4 * NA;  // act loads of a block
+  // entries: experts, those of many tokens several times; place of its tokens among the members, expert, tokens
+  __shared__ int s_ids[MAXP], s_first[MAXP], s_ad[kFewTokens], s_lead[MAXP], s_expert[MAXP], s_n;
+  __shared__ uint8_t s_m[MAXP];
   __shared__ float s_w[MAXP];
   __shared__ int16_t s_pair[MAXP * C];  // of an entry's column: its token's first pair with the expert, or -1
   __shared__ float s_wt[MAXP * C];      // and the sum of its weights
-  __shared__ __attribute__((aligned(16))) float s_z[NW][64];
-  __shared__ float s_sum[NW][kFewTokens][16];
+  __shared__ __attribute__((aligned(16))) float s_z[NW][4][64];
+  __shared__ float s_sum[NW][kFewTokens][FT];
+  __shared__ __attribute__((aligned(16))) uint8_t s_act[NW][AL * 1024];  // rows (part of a step, token, half) of 128
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, kq = lane >> 4;
   const int T = a.T, k = a.k, K = a.I, r = a.r, P = T * k, h = a.h;
@@ -358,17 +410,27 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
     s_ids[i] = a.ids[i];
     s_w[i] = a.w[i];
   }
-  for (int i = lane; i < kFewTokens * 16; i += 64) s_sum[wave][i / 16][i % 16] = 0.f;
-  int n_lead = 0;
-  if (wave == 0) {  // the pairs that stand for an expert
-    int flags = 0;
+  if (tid < T) s_ad[tid] = sanitize_adapter(a.adapter_ids[tid], a.nA);
+  for (int i = lane; i < kFewTokens * FT; i += 64) s_sum[wave][i / FT][i % FT] = 0.f;
+  if (wave == 0) {  // the pairs that stand for an expert, and their entries
+    int n = 0, flags = 0;
     for (int i = 0; i < P; i += 64) {
-      const bool lead = i + lane < P && a.lead[i + lane] != 0;
-      if (i + lane < P) flags |= a.pair_flags[i + lane];
-      const uint64_t all = __ballot(lead);
-      if (lead) s_lead[n_lead + (int)__popcll(all & lanemask_lt())] = i + lane;
-      n_lead += (int)__popcll(all);
+      const int p = i + lane, tokens = p < P ? a.members[p] : 0, entries = (tokens + C - 1) / C;
+      if (p < P) flags |= a.pair_flags[p];
+      int before = 0, all = 0;  // entries of the lanes before, and of all
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        const uint64_t has = __ballot((entries >> b) & 1);
+        before += (int)__popcll(has & lanemask_lt()) << b;
+        all += (int)__popcll(has) << b;
+      }
+      for (int q = 0; q < entries; ++q) {
+        s_lead[n + before + q] = p * kFewTokens + q * C;
+        s_m[n + before + q] = (uint8_t)min(tokens - q * C, C);
+      }
+      n += all;
     }
+    if (lane == 0) s_n = n;
     if (blockIdx.x == 0) {
 #pragma unroll
       for (int b = 1; b <= 4; b *= 2) {
@@ -379,148 +441,171 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
     }
   }
   __syncthreads();
-  if (wave == 0) {  // their entries
-    int n = 0;
-    for (int i = 0; i < n_lead; i += 64) {
-      const bool in = i + lane < n_lead;
-      const int e = in ? s_ids[s_lead[i + lane]] : -2;
-      int tokens = 0;
-      if (in && T > C)
-        for (int t = 0; t < T; ++t) {
-          bool has = false;
-          for (int j = 0; j < k; ++j) has |= s_ids[t * k + j] == e;
-          tokens += has;
-        }
-      const bool twice = tokens > C;
-      const uint64_t more = __ballot(twice);
-      if (in) {
-        const int at = n + lane + (int)__popcll(more & lanemask_lt());
-        s_expert[at] = e;
-        s_part[at] = 0;
-        if (twice) {
-          s_expert[at + 1] = e;
-          s_part[at + 1] = 1;
-        }
-      }
-      n += min(64, n_lead - i) + (int)__popcll(more);
-    }
-    if (lane == 0) s_n = n;
-  }
-  __syncthreads();
   const int U = s_n;
   for (int i = tid; i < U * C; i += NTH) {
-    const int e = s_expert[i / C];
-    int left = i % C + C * s_part[i / C], pair = -1;  // the token with so many of the expert's before it
-    float w = 0.f;
-    for (int t = 0; t < T && pair < 0; ++t) {
-      int first = -1;
-      for (int j = k - 1; j >= 0; --j)
-        if (s_ids[t * k + j] == e) first = t * k + j;
-      if (first >= 0 && left-- == 0) pair = first;
-    }
-    if (pair >= 0)
-      for (int p = pair; p < (pair / k + 1) * k; ++p)
-        if (s_ids[p] == e) w += s_w[p];
-    s_pair[i] = (int16_t)pair;
-    s_wt[i] = w;
+    const int u = i / C, c = i % C;
+    const bool in = c < s_m[u];
+    s_pair[i] = in ? (int16_t)a.member_pair[s_lead[u] + c] : (int16_t)-1;
+    s_wt[i] = in ? a.member_w[s_lead[u] + c] : 0.f;
+    if (c == 0) s_expert[u] = s_ids[s_lead[u] / kFewTokens];
+  }
+  for (int p = tid; p < P; p += NTH) {  // the token's first pair with the expert holds z2's parts
+    int first = p;
+    for (int q = p - 1; q >= p / k * k; --q)
+      if (s_ids[q] == s_ids[p]) first = q;
+    s_first[p] = first;
   }
   __syncthreads();
 
-  const int nch = K / 128, total = U * nch;
+  // Steps i0 .. i1 - 1 of this wavefront: entry i / nch, K step i % nch.
+  const int nk = K / 128, nch = (nk + SUB - 1) / SUB, total = U * nch;
   const int i0 = (int)((int64_t)total * wave / NW), i1 = (int)((int64_t)total * (wave + 1) / NW);
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.act, 0x7fffffffu);
   struct Set {
-    u32x4 w[WL], act[NA][4];
-    f32x4 scale;
+    u32x4 w[WL];
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  const int row_m = FT == 8 ? m & 7 : m, sub_m = FT == 8 ? m >> 3 : 0;  // the lane's feature and part of a step
   auto load = [&](Set& s, int i) {
-    const bool in = i < i1;
-    const int u = in ? i / nch : 0, step = i - u * nch;
-    const int e = in ? __builtin_amdgcn_readfirstlane(s_expert[u]) : 0;
+    const int u = i < i1 ? i / nch : 0, step = (i - u * nch) * SUB + sub_m;
+    const bool in = i < i1 && step < nk;
+    const int e = i < i1 ? __builtin_amdgcn_readfirstlane(s_expert[u]) : 0;
     const __amdgpu_buffer_rsrc_t wr = make_rsrc((const uint8_t*)a.W2 + ((int64_t)e * h + n0) * K * WB, 0x7fffffffu);
-    const bool row = in && (FT == 16 || m < FT);
 #pragma unroll
     for (int j = 0; j < WL; ++j)
-      s.w[j] = bufld16(wr, row ? (uint32_t)((m * K + step * 128 + few_k<W8>(W8 ? 2 * j : j, kq)) * WB) : kOutOfRange);
-#pragma unroll
-    for (int p = 0; p < NA; ++p) {
-      const int pair = in ? s_pair[u * C + 8 * p + (m & 7)] : -1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s.act[p][j] = bufld16(ar, pair >= 0 ? (uint32_t)(((pair * 2 + (m >> 3)) * K + step * 128 + few_k<W8>(j, kq)) * 2)
-                                            : kOutOfRange);
-    }
-    if (W8) s.scale = FT == 16 || kq < FT / 4 ? *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)e * h + n0 + 4 * kq) : zero;
+      s.w[j] = bufld16(wr, in ? (uint32_t)((row_m * K + step * 128 + few_k<W8>(W8 ? 2 * j : j, kq)) * WB) : kOutOfRange);
   };
   Set set[NS];
 #pragma unroll
   for (int q = 0; q < NS - 1; ++q) load(set[q], i0 + q);
-
-  const int per = r / 4;                       // lanes of a tile's part of z2, 4 values each
-  const int at = lane / per, step = 64 / per;  // first tile and tiles at once
-  const int q4 = (lane - at * per) * 4;
-  for (int p = wave; p < P; p += NW) {
-    const int e = s_ids[p], t = p / k;
-    const int ad = sanitize_adapter(a.adapter_ids[t], a.nA);
-    if (e < 0 || ad < 0) continue;
-    int first = p;  // the token's first pair with this expert holds z2's parts
-    for (int q = p - 1; q >= t * k; --q)
-      if (s_ids[q] == e) first = q;
-    // lanes 4 n ..: feature n0 + n, a quarter of the ranks each
-    const int n = lane >> 2, q0 = (lane & 3) * per;
-    const uint16_t* b = a.B2 + (((int64_t)ad * a.E + e) * h + n0 + n) * r + q0;
-    uint32_t bv[8];
+  // A block: the steps from i on, of one entry, whose act fits the region.
+  auto block_steps = [&](int i) {
+    const int u = i / nch;
+    return min(min(AL * 2 / (s_m[u] * SUB), nch - (i - u * nch)), i1 - i);
+  };
+  u32x4 next[AL];
+  auto load_act = [&](int i) {  // of the block that begins at step i: 16-byte chunks, row by row
+    const bool in = i < i1;
+    const int u = in ? i / nch : 0, step = (i - u * nch) * SUB;
+    const int M = in ? __builtin_amdgcn_readfirstlane(s_m[u]) : 1, rows = in ? block_steps(i) * SUB * M * 2 : 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) bv[q] = 2 * q < per && n < FT ? *reinterpret_cast<const uint32_t*>(b + 2 * q) : 0u;
-    // z2: a lane adds every step-th tile's part, then lanes meet (per is a power of two)
-    const float* parts = a.zpart + (int64_t)first * a.tiles * r + q4;
-    f32x4 z = zero;
-    for (int i = at; i < a.tiles; i += 8 * step) {
-      f32x4 v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        v[q] = i + q * step < a.tiles ? *reinterpret_cast<const f32x4*>(parts + (int64_t)(i + q * step) * r) : zero;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) z += v[q];
+    for (int q = 0; q < AL; ++q) {
+      const int row = q * 4 + (lane >> 4), g = row / (2 * M), c = (row - g * 2 * M) >> 1;
+      const bool ok = row < rows && step + g < nk;
+      const int pair = ok ? s_pair[u * C + c] : 0;
+      next[q] = bufld16(ar, ok ? (uint32_t)(((pair * 2 + (row & 1)) * K + (step + g) * 128 + 8 * m) * 2) : kOutOfRange);
     }
-    for (int d = per; d < 64; d *= 2)
+  };
+  load_act(i0);
+
+  // The adapters' term: a pair on 16 lanes, four pairs a wavefront at once; of few pairs several lane groups take
+  // some tiles' parts each (the term is linear in z2). A lane adds every step-th tile's part of four ranks, the
+  // lanes of a rank meet, then each lane has a feature (FT = 8: half of its ranks).
+  {
+    const int slots = 4 * NW, quarter = lane >> 4;
+    int shares = 1;
+    while (shares * 2 * P <= slots) shares *= 2;
+    const int per = r / 4, step = 16 / per, at = m / per, q4 = (m - at * per) * 4;
+    const int n = m % FT, half = m / FT, nb = FT == 8 ? 2 : 1;
+    for (int w0 = 0; w0 < P * shares; w0 += slots) {
+      const int w = w0 + quarter * NW + wave;
+      const bool in = w < P * shares;
+      const int p = in ? w / shares : 0, share = w - p * shares, tok = p / k, e = s_ids[p];
+      const bool on = in && e >= 0 && s_ad[tok] >= 0;
+      const uint16_t* const b = a.B2 + (((int64_t)s_ad[tok] * a.E + e) * h + n0 + n) * r;
+      u32x4 bv[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] += __shfl_xor(z[c], d);
-    if (lane < per) *reinterpret_cast<f32x4*>(&s_z[wave][q4]) = z;
-    __builtin_amdgcn_wave_barrier();
-    float s = 0.f;
+      for (int q = 0; q < 4; ++q) bv[q] = on && 8 * (q * nb + half) < r ? ldg16(b + 8 * (q * nb + half)) : u32x4{0u, 0u, 0u, 0u};
+      const float* const parts = a.zpart + (int64_t)s_first[p] * a.tiles * r + q4;
+      const int last = on ? a.tiles * (share + 1) / shares : 0;
+      f32x4 z = zero;
+      for (int i = a.tiles * share / shares + at; i < last; i += 3 * step) {
+        f32x4 v[3];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (2 * q < per) s += s_z[wave][q0 + 2 * q] * bf16_lo(bv[q]) + s_z[wave][q0 + 2 * q + 1] * bf16_hi(bv[q]);
-    s += __shfl_xor(s, 1);
-    s += __shfl_xor(s, 2);
-    if ((lane & 3) == 0 && n < FT) s_sum[wave][t][n] += s_w[p] * s;
-    __builtin_amdgcn_wave_barrier();
+        for (int q = 0; q < 3; ++q)
+          v[q] = i + q * step < last ? *reinterpret_cast<const f32x4*>(parts + (int64_t)(i + q * step) * r) : zero;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) z += v[q];
+      }
+      for (int d = per; d < 16; d *= 2)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[c] += __shfl_xor(z[c], d);
+      if (at == 0) *reinterpret_cast<f32x4*>(&s_z[wave][quarter][q4]) = z;
+      __builtin_amdgcn_wave_barrier();
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8 / nb; ++q) {
+        const int q0 = 8 * (q * nb + half);
+        if (q0 >= r) continue;
+        const u32x4 bq = q < 4 ? bv[q & 3] : on ? ldg16(b + q0) : u32x4{0u, 0u, 0u, 0u};
+        s += dot8(bq, &s_z[wave][quarter][q0]);
+      }
+      if (FT == 8) s += __shfl_xor(s, 8);
+      // (pairs of one token among the four: one after another)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (quarter == q && on && half == 0) s_sum[wave][tok][n] += s_w[p] * s;
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
 
   f32x4 acc[NA];
 #pragma unroll
   for (int p = 0; p < NA; ++p) acc[p] = zero;
+  uint8_t* const own = s_act[wave];
+  int begin = 0, end = i0, M = 1;  // the block in LDS, its entry's tokens
   auto compute = [&](const Set& s, int i) {
+    if (i == end && i < i1) {
+      // (LDS accesses of a wavefront keep their order; the barriers keep the compiler from changing it)
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int q = 0; q < AL; ++q) {
+        const int row = q * 4 + (lane >> 4);
+        *reinterpret_cast<u32x4*>(own + row * 256 + (m ^ (row & 15)) * 16) = next[q];
+      }
+      __builtin_amdgcn_wave_barrier();
+      begin = i;
+      M = __builtin_amdgcn_readfirstlane(s_m[i / nch]);
+      end = i + __builtin_amdgcn_readfirstlane(block_steps(i));
+      load_act(end);
+    }
+    // (columns past the entry's tokens hold another token's, and are not read; steps past the end have zeros for
+    // weights)
+    const int g = (min(i, end - 1) - begin) * SUB + sub_m;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const u32x4 wv = W8 ? e4m3x8_to_bf16(s.w[j / 2 % WL], j % 2) : s.w[j % WL];
 #pragma unroll
-      for (int p = 0; p < NA; ++p) acc[p] = mfma16(wv, s.act[p][j], acc[p]);
+      for (int p = 0; p < NA; ++p) {
+        const int c = FT == 8 ? m & 3 : (m & 7) + 8 * p, part = FT == 8 ? (m >> 2) & 1 : m >> 3;
+        const int row = (g * M + min(c, M - 1)) * 2 + part, chunk = few_k<W8>(j, kq) / 8;
+        acc[p] = mfma16(wv, *reinterpret_cast<const u32x4*>(own + row * 256 + (chunk ^ (row & 15)) * 16), acc[p]);
+      }
     }
     const int u = i / nch;
     if (i < i1 && (i == i1 - 1 || i - u * nch == nch - 1)) {  // this wavefront's last step of the expert
+      const int kf = FT == 8 ? kq & 1 : kq;  // features 4 kf ..
+      f32x4 scale = {1.f, 1.f, 1.f, 1.f};
+      if (W8) scale = *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)s_expert[u] * h + n0 + 4 * kf);
 #pragma unroll
       for (int p = 0; p < NA; ++p) {
-        const int pair = s_pair[u * C + 8 * p + (m & 7)];
-        const float w = s_wt[u * C + 8 * p + (m & 7)];
+        const int c = FT == 8 ? m & 3 : (m & 7) + 8 * p;
+        const int pair = s_pair[u * C + c];
+        const float w = s_wt[u * C + c];
+        const bool mine = pair >= 0 && (FT == 8 ? kq < 2 && m < 4 : m < 8);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float v = acc[p][c] + __shfl_xor(acc[p][c], 8);
-          if (pair >= 0 && m < 8) s_sum[wave][pair / k][4 * kq + c] += w * (W8 ? v * s.scale[c] : v);
-          acc[p][c] = 0.f;
+        for (int f = 0; f < 4; ++f) {
+          float v = acc[p][f];
+          if (FT == 8) {
+            v += __shfl_xor(v, 4);   // high and low
+            v += __shfl_xor(v, 40);  // the halves of the steps: rows and columns 8 further
+          } else {
+            v += __shfl_xor(v, 8);
+          }
+          if (mine) s_sum[wave][pair / k][4 * kf + f] += w * (v * scale[f]);
+          acc[p][f] = 0.f;
         }
       }
     }
@@ -550,7 +635,7 @@ namespace {
 
 template <int FT, int NA>
 void launch_down(const FewArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.h / FT)), block(64 * kFewDownWaves);
+  const dim3 grid((unsigned)(a.h / FT)), block(64 * (kFewDownWaves / NA));
   if (a.s1) hipLaunchKernelGGL((few_down_kernel<FT, NA, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((few_down_kernel<FT, NA, false>), grid, block, 0, stream, a);
 }
@@ -581,11 +666,11 @@ hipError_t launch_few(const FewArgs& a, int ct, hipStream_t stream) {
 #undef MOELORA_FEW
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // 8 features a workgroup where 16 would leave CUs without one; two products a step where experts have more
-  // than 4 tokens on average
-  const bool two = a.T > 8 && P > 4 * a.E, narrow = a.h / 16 < 256;
-  if (two) narrow ? launch_down<8, 2>(a, stream) : launch_down<16, 2>(a, stream);
-  else narrow ? launch_down<8, 1>(a, stream) : launch_down<16, 1>(a, stream);
+  // two products a step where experts have more than 4 tokens on average; 8 features a workgroup where 16 leave
+  // CUs without one, unless experts have more tokens than its steps have columns for
+  if (a.T > 8 && P > 4 * a.E) launch_down<16, 2>(a, stream);
+  else if (a.h / 16 < 256 && (a.T <= 4 || P <= 2 * a.E)) launch_down<8, 1>(a, stream);
+  else launch_down<16, 1>(a, stream);
   return hipGetLastError();
 }
 

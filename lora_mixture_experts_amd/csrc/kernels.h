@@ -262,7 +262,9 @@ struct FewArgs {
   int* ids;         // [P] expert, -1 for an empty slot
   float* w;         // [P]
   int* pair_flags;  // [P]
-  int* lead;        // [P]: 1 for the first pair that names its expert
+  int* members;     // [P]: tokens of its expert for the first pair that names it, else 0
+  int* member_pair; // [P][16]: of such a pair: these tokens' first pairs with the expert, in token order
+  float* member_w;  // [P][16]: and the sums of their weights
   float* z1;        // [z_splits][P][r], added in this order
   int z_splits;
   uint16_t* act;    // [P][2][I]: high and low parts
