@@ -120,8 +120,7 @@ struct AdapterRows {
     }
   }
   template <int NB>
-  __device__ __forceinline__ void load_first(const LinearArgs& a, int t0, int part, int parts, int lane) {
-    if (part >= n) return;
+  __device__ __forceinline__ void load_z(const LinearArgs& a, int t0, int lane) {
     const int fg = lane >> 5;
     // (rank 8: the two halves of the wavefront hold high and low of the same ranks)
 #pragma unroll
@@ -133,16 +132,18 @@ struct AdapterRows {
       }
       __builtin_amdgcn_sched_barrier(0);  // (one operand's parts in registers at a time)
     }
-    load_b<NB>(a, part, parts);
   }
-  __device__ __forceinline__ void load_first(const LinearArgs& a, int t0, int part, int parts, int lane) {
-    if (a.r <= 16) load_first<1>(a, t0, part, parts, lane);
-    else if (a.r == 32) load_first<2>(a, t0, part, parts, lane);
-    else load_first<4>(a, t0, part, parts, lane);
+  __device__ __forceinline__ void load_first(const LinearArgs& a, int part, int parts) {
+    if (part >= n) return;
+    if (a.r <= 16) load_b<1>(a, part, parts);
+    else if (a.r == 32) load_b<2>(a, part, parts);
+    else load_b<4>(a, part, parts);
   }
   template <int NB>
-  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int part, int parts, int lane) {
+  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int t0, int part, int parts, int lane) {
     constexpr int D = kOperands / (FN * NB);
+    if (part >= n) return;
+    load_z<NB>(a, t0, lane);
     for (int i = part; i < n; i += D * parts) {
       if (i != part) load_b<NB>(a, i, parts);
 #pragma unroll
@@ -174,10 +175,10 @@ struct AdapterRows {
       }
     }
   }
-  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int part, int parts, int lane) {
-    if (a.r <= 16) add<1>(acc, a, part, parts, lane);
-    else if (a.r == 32) add<2>(acc, a, part, parts, lane);
-    else add<4>(acc, a, part, parts, lane);
+  __device__ __forceinline__ void add(f32x16 (&acc)[FN], const LinearArgs& a, int t0, int part, int parts, int lane) {
+    if (a.r <= 16) add<1>(acc, a, t0, part, parts, lane);
+    else if (a.r == 32) add<2>(acc, a, t0, part, parts, lane);
+    else add<4>(acc, a, t0, part, parts, lane);
   }
 };
 
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   Pipe::run_steps(acc, ld, lds + kg * (Pipe::LDS_BYTES / 2), nsteps, wave, lane, [&] {
-    if constexpr (LORA && FM == 1) rows_ad.load_first(a, row0 + wm * WM, part, parts, lane);
+    if constexpr (LORA && FM == 1) rows_ad.load_first(a, part, parts);
   });
 
   if constexpr (LORA) {  // (the adapters' term takes no weight scale)
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[i][j][v] *= sc[j];
     }
-    if constexpr (FM == 1) rows_ad.add(acc[0], a, part, parts, lane);
+    if constexpr (FM == 1) rows_ad.add(acc[0], a, row0 + wm * WM, part, parts, lane);
     else add_adapters_tile<BM, BN, NWV, FM, FN>(acc, a, row0, wm * WM, wn * WN, wrow_of, lds, part, parts, wave, lane);
 #pragma unroll
     for (int j = 0; j < FN; ++j) sc[j] = 1.f;
