@@ -31,24 +31,22 @@ struct LoraLayout {
   size_t z, groups, part, total;
 };
 
-// Workgroups of the shrink: `slots` that share the adapters of 32 tokens, `splits` that share K (not below 512
-// of it). Up to 512 tokens may all be of different requests; more are prompts, where most of 32 tokens have
-// one adapter and a third workgroup finds nothing to do. K is split where that leaves CUs idle. Measured (us,
-// K = 4096): 64 tokens of 8 adapters, 8 slots, 1 to 8 splits 9.0 6.2 4.8 4.5; 256 tokens of 64, 32 slots 11.4
-// 10.0 15.4 26.2, 8 slots 28.2 18.1 12.9 14.2; 1024 tokens in runs, 4 slots 13.3 8.2 5.6 6.8; 4096 in runs, rank
-// 64, 4 slots 24.3 26.8 25.7 41.3, 32 slots 33.6 53.0.
+// The shrink's form: adapter by adapter (slots = 0) for batches, whose tokens may all be of different requests,
+// else 32 tokens after another, with four workgroups for their adapters (prompts mostly have one). K is split (not
+// below 512 of it) where that leaves CUs idle.
 struct ShrinkPlan {
   int slots, splits;
 };
 
 ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
-  const int T = d->linear.T, groups = std::max(1, (T + 31) / 32);
+  const moe_lora_linear_dims& l = d->linear;
+  const int groups = std::max(1, (l.T + 31) / 32);
   ShrinkPlan p;
-  p.slots = std::max(1, std::min({T <= 512 ? 32 : 4, T, d->n_adapters}));
-  const int busy = groups * (T <= 512 ? p.slots : 1);
+  const bool batch = l.T <= kAdapterShrinkTokens && d->n_adapters <= 1024 && l.T * l.x_stride * 2 < ((int64_t)1 << 31);
+  p.slots = batch ? 0 : std::min({4, std::max(l.T, 1), d->n_adapters});
+  const int busy = batch ? std::max(1, std::min(l.T, d->n_adapters)) : groups, enough = batch ? 257 : 128;
   p.splits = 1;
-  const int few = T <= 512 ? 257 : 128;  // busy workgroups
-  while (p.splits < 8 && busy * p.splits < few && d->linear.in_features >= 1024 * p.splits) p.splits *= 2;
+  while (p.splits < 8 && busy * p.splits < enough && l.in_features >= 1024 * p.splits) p.splits *= 2;
   return p;
 }
 

@@ -177,6 +177,7 @@ struct TokenAdapters {
   uint32_t tokens[32];  // bit i: token i of the 32
 };
 
+constexpr int kAdapterShrinkTokens = 512;  // tokens of a batch whose shrink goes adapter by adapter
 // LoRA shrink of tokens in their own order: z = x A_a^T for the projection with adapters, and the
 // adapters of every 32 tokens.
 struct TokenShrinkArgs {
@@ -187,7 +188,7 @@ struct TokenShrinkArgs {
   int T, K, nA, r;
   float* z;  // [splits][T][r]: sums of each split of K, rows without an adapter unwritten
   TokenAdapters* groups;  // [ceil(T / 32)]
-  int slots;   // workgroups that share the adapters of 32 tokens
+  int slots;   // workgroups that share the adapters of 32 tokens; 0: a workgroup an adapter
   int splits;  // workgroups that share K: 1, 2, 4 or 8
 };
 

@@ -127,24 +127,37 @@ __device__ __forceinline__ float low_part(float v, float high) {
   return fabsf(d) < INFINITY ? d : 0.f;
 }
 
+__device__ __forceinline__ void split_operands(f32x4 v0, f32x4 v1, u32x4& high, u32x4& low) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = i < 2 ? v0[2 * i] : v1[2 * i - 4], y = i < 2 ? v0[2 * i + 1] : v1[2 * i - 3];
+    h[i] = to_bf16x2(x, y);
+    l[i] = to_bf16x2(low_part(x, bf16_lo(h[i])), low_part(y, bf16_hi(h[i])));
+  }
+  high = u32x4{h[0], h[1], h[2], h[3]};
+  low = u32x4{l[0], l[1], l[2], l[3]};
+}
+
+// Eight values of z: its S splits, added in their order.
 template <int S>
-__device__ __forceinline__ void z_sum(float (&v)[8], const float* z, int64_t split) {
+__device__ __forceinline__ void z_sum(f32x4 (&v)[2], const float* z, int64_t split) {
   f32x4 p[S][2];
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int i = 0; i < 2; ++i) p[s][i] = *reinterpret_cast<const f32x4*>(z + s * split + 4 * i);
 #pragma unroll
-  for (int s = 1; s < S; ++s)
+  for (int i = 0; i < 2; ++i) {
+    v[i] = p[0][i];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) p[0][i] += p[s][i];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = p[0][i / 4][i % 4];
+    for (int s = 1; s < S; ++s) v[i] += p[s][i];
+  }
 }
 
 // z of token t, ranks q .. q + 7, as high and low operands (zeros for a token past the end).
 __device__ __forceinline__ void z_operands(const LinearArgs& a, int t, int q, u32x4& high, u32x4& low) {
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   if (t < a.T) {
     const float* z = a.z + (int64_t)t * a.r + q;
     const int64_t split = (int64_t)a.T * a.r;
@@ -153,14 +166,7 @@ __device__ __forceinline__ void z_operands(const LinearArgs& a, int t, int q, u3
     else if (a.z_splits == 4) z_sum<4>(v, z, split);
     else z_sum<8>(v, z, split);
   }
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = to_bf16x2(v[2 * i], v[2 * i + 1]);
-    l[i] = to_bf16x2(low_part(v[2 * i], bf16_lo(h[i])), low_part(v[2 * i + 1], bf16_hi(h[i])));
-  }
-  high = u32x4{h[0], h[1], h[2], h[3]};
-  low = u32x4{l[0], l[1], l[2], l[3]};
+  split_operands(v[0], v[1], high, low);
 }
 
 // The flag of moe_lora_debug_status for a call with adapters: one wavefront, once every group is written.

@@ -16,17 +16,43 @@
 
 namespace moelora {
 
-// Shrink. A workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
-// index `slot`, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (no
-// sort by adapter: the tokens of a prompt lie together anyway, and those of a decode batch are mostly of
-// different requests). 16x16x32 MFMAs with the rows of A on their A side and 16 tokens on their B side;
-// tokens without the adapter load zeros, which costs no traffic, and their sums are dropped. The eight
-// wavefronts take the 64-wide K chunks in turn, two in flight, and their sums meet in LDS in wavefront
-// order, in fp32.
-// NQ: 16-row tiles of A (rank 8 and 16: 1, 32: 2, 64: 4). NT: 16-token tiles.
-template <int NQ, int NT>
+// The adapters of 32 consecutive tokens, by one wavefront.
+__device__ __forceinline__ void write_group(const TokenShrinkArgs& a, int group, int ad, bool bad) {
+  TokenAdapters* const grp = a.groups + group;
+  uint32_t left = (uint32_t)__ballot(ad >= 0);
+  int n = 0;
+  while (left) {
+    const int one = __builtin_amdgcn_readlane(ad, __builtin_ctz(left));
+    const uint32_t who = (uint32_t)__ballot(ad == one) & left;
+    left &= ~who;
+    if ((threadIdx.x & 63) == 0) {
+      grp->adapter[n] = one;
+      grp->tokens[n] = who;
+    }
+    ++n;
+  }
+  if ((threadIdx.x & 63) == 0) {
+    grp->n = n;
+    grp->bad = bad;
+  }
+}
+
+// The id of token t0 + lane of 32 (-1: none), and whether one of them is out of range.
+__device__ __forceinline__ int adapter_of(const TokenShrinkArgs& a, int t0, int lane, bool& bad) {
+  const int given = lane < 32 && t0 + lane < a.T ? a.adapter_ids[t0 + lane] : -1;
+  const int ad = sanitize_adapter(given, a.nA);
+  bad = __ballot(given != ad && given != -1) != 0;
+  return ad;
+}
+
+// Shrink of prompts: a workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
+// index `slot`, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (the tokens of a
+// prompt lie together, no sort is needed). Tokens without the adapter load zeros, which costs no traffic, and
+// their sums are dropped.
+// NQ: 16-row tiles of A (rank 8 and 16: 1, 32: 2, 64: 4).
+template <int NQ>
 __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenShrinkArgs a) {
-  constexpr int WK = kShrinkWaves;
+  constexpr int WK = kShrinkWaves, NT = 2;
   const int lane = threadIdx.x & 63;
   const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kq = lane >> 4;
@@ -44,13 +70,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
     if (i / a.splits >= per || group >= groups) return;
   }
   const int t0 = group * 32, K = a.K, r = a.r;
-
-  // the group's adapters, found by every wavefront for itself
-  const int given = lane < 32 && t0 + lane < a.T ? a.adapter_ids[t0 + lane] : -1;
-  const int ad = sanitize_adapter(given, a.nA);
-  const bool bad = __ballot(given != ad && given != -1) != 0;
-  TokenAdapters* const grp = a.groups + group;
-  const bool writes = slot == 0 && sp == 0 && wk == 0;
+  bool bad;
+  const int ad = adapter_of(a, t0, lane, bad);  // (by every wavefront for itself)
+  if (slot == 0 && sp == 0 && wk == 0) write_group(a, group, ad, bad);
   // this split's K range, in whole 64-wide chunks
   const int chunks = (K + 63) / 64;
   const int k0 = chunks * sp / a.splits * 64, k1 = min(K, chunks * (sp + 1) / a.splits * 64);
@@ -58,17 +80,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
   __shared__ f32x4 part[WK][NQ][NT][64];
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X + (int64_t)t0 * a.ldx, 0x7fffffffu);
   uint32_t left = (uint32_t)__ballot(ad >= 0);
-  int n = 0;
-  while (left) {
+  for (int n = 0; left; ++n) {
     const int one = __builtin_amdgcn_readlane(ad, __builtin_ctz(left));
     const uint32_t who = (uint32_t)__ballot(ad == one) & left;
     left &= ~who;
-    const int index = n++;
-    if (writes && lane == 0) {
-      grp->adapter[index] = one;
-      grp->tokens[index] = who;
-    }
-    if (index % a.slots != slot) continue;
+    if (n % a.slots != slot) continue;
     const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.A + (int64_t)one * r * K, (uint32_t)((size_t)r * K * 2));
     uint32_t ao[NQ], xo[NT];
 #pragma unroll
@@ -87,32 +103,84 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
         *reinterpret_cast<f32x4*>(a.z + ((int64_t)sp * a.T + t0 + nt * 16 + m) * r + q) = sum;
     }
   }
-  if (writes && lane == 0) {
-    grp->n = n;
-    grp->bad = bad;
+}
+
+// Shrink of batches, whose tokens are mostly of different requests: a workgroup an adapter (blockIdx.y) and split
+// of K, which looks its tokens up among all ids, so that A is read once (by 32 tokens as above, 256 tokens of 64
+// adapters read it three times: 10.5 us). The workgroups behind the last adapter write the tokens' groups.
+template <int NQ>
+__global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(TokenShrinkArgs a) {
+  constexpr int WK = kShrinkWaves;
+  __shared__ f32x4 part[WK][NQ][1][64];
+  __shared__ int s_tok[kAdapterShrinkTokens], s_n[kAdapterShrinkTokens / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wk = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 15, kq = lane >> 4;
+  const int one = blockIdx.y, sp = blockIdx.x, K = a.K, r = a.r;
+  if (one >= a.nA) {
+    const int group = (one - a.nA) * WK + wk;
+    if (sp != 0 || group >= (a.T + 31) / 32) return;
+    bool bad;
+    const int ad = adapter_of(a, group * 32, lane, bad);
+    write_group(a, group, ad, bad);
+    return;
+  }
+  // the adapter's tokens in order: wavefront w looks at tokens 64 w ..
+  static_assert(kAdapterShrinkTokens == 64 * WK, "a token a thread");
+  const bool mine = tid < a.T && a.adapter_ids[tid] == one;
+  const uint64_t all = __ballot(mine);
+  if (lane == 0) s_n[wk] = (int)__popcll(all);
+  __syncthreads();
+  int before = 0, n = 0;
+#pragma unroll
+  for (int w = 0; w < WK; ++w) {
+    if (w < wk) before += s_n[w];
+    n += s_n[w];
+  }
+  if (n == 0) return;
+  if (mine) s_tok[before + (int)__popcll(all & lanemask_lt())] = tid;
+  __syncthreads();
+  const int chunks = (K + 63) / 64;
+  const int k0 = chunks * sp / a.splits * 64, k1 = min(K, chunks * (sp + 1) / a.splits * 64);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, 0x7fffffffu);
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.A + (int64_t)one * r * K, (uint32_t)((size_t)r * K * 2));
+  uint32_t ao[NQ];
+#pragma unroll
+  for (int c = 0; c < NQ; ++c) ao[c] = c * 16 + m < r ? (uint32_t)((size_t)(c * 16 + m) * K * 2) : kOutOfRange;
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    const int tok = i0 + m < n ? s_tok[i0 + m] : -1;
+    const uint32_t xo[1] = {tok >= 0 ? (uint32_t)(tok * a.ldx * 2) : kOutOfRange};
+    shrink_rows<NQ, 1>(part, ar, ao, xr, xo, k0, k1, wk, lane);
+    // lane: z columns 16 c + 4 kq .. + 3 of the chunk's token m
+    const int q = 16 * wk + 4 * kq;
+    if (wk < NQ && q < r && tok >= 0) {
+      f32x4 sum = part[0][wk][0][lane];
+#pragma unroll
+      for (int p = 1; p < WK; ++p) sum += part[p][wk][0][lane];
+      *reinterpret_cast<f32x4*>(a.z + ((int64_t)sp * a.T + tok) * r + q) = sum;
+    }
   }
 }
 
 hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream) {
   if (a.T <= 0) return hipSuccess;
-  if (a.slots < 1 || a.slots > 32 || a.splits < 1 || a.splits > 8 || a.K % 8 != 0) return hipErrorInvalidValue;
+  if (a.slots < 0 || a.slots > 32 || a.splits < 1 || a.splits > 8 || a.K % 8 != 0) return hipErrorInvalidValue;
   const int groups = (a.T + 31) / 32;
-  const dim3 grid((unsigned)((groups < 8 ? groups : (groups + 7) / 8 * 8) * a.splits), (unsigned)a.slots);
   const dim3 block(64 * kShrinkWaves);
-  const bool one = a.T <= 16;
-#define MOELORA_TOKEN_SHRINK(NQ_)                                                              \
-  if (one) hipLaunchKernelGGL((token_shrink_kernel<NQ_, 1>), grid, block, 0, stream, a);       \
-  else hipLaunchKernelGGL((token_shrink_kernel<NQ_, 2>), grid, block, 0, stream, a)
-  if (a.r == 8 || a.r == 16) {
-    MOELORA_TOKEN_SHRINK(1);
-  } else if (a.r == 32) {
-    MOELORA_TOKEN_SHRINK(2);
-  } else if (a.r == 64) {
-    MOELORA_TOKEN_SHRINK(4);
-  } else {
-    return hipErrorInvalidValue;
+  if (a.slots == 0) {
+    if (a.T > kAdapterShrinkTokens || (int64_t)a.T * a.ldx * 2 >= (int64_t)kOutOfRange) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)a.splits, (unsigned)(a.nA + (groups + kShrinkWaves - 1) / kShrinkWaves));
+    if (a.r == 8 || a.r == 16) hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, block, 0, stream, a);
+    else if (a.r == 32) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, block, 0, stream, a);
+    else if (a.r == 64) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, block, 0, stream, a);
+    else return hipErrorInvalidValue;
+    return hipGetLastError();
   }
-#undef MOELORA_TOKEN_SHRINK
+  const dim3 grid((unsigned)((groups < 8 ? groups : (groups + 7) / 8 * 8) * a.splits), (unsigned)a.slots);
+  if (a.r == 8 || a.r == 16) hipLaunchKernelGGL(token_shrink_kernel<1>, grid, block, 0, stream, a);
+  else if (a.r == 32) hipLaunchKernelGGL(token_shrink_kernel<2>, grid, block, 0, stream, a);
+  else if (a.r == 64) hipLaunchKernelGGL(token_shrink_kernel<4>, grid, block, 0, stream, a);
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 

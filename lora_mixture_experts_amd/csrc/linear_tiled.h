@@ -255,10 +255,30 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
   if (one < 0) return;
   __syncthreads();  // (the stages are free)
   load(one, 0);
-  for (int i = threadIdx.x; i < BM * bc; i += 64 * NWV) {
-    const int row = i / bc, c = i - row * bc;
+  // z of the tile's rows, up to four chunks of eight ranks a thread, all loaded before the first is stored
+  constexpr int NZ = BM * 8 / (64 * NWV);
+  f32x4 z8[NZ][2];
+#pragma unroll
+  for (int q = 0; q < NZ; ++q)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) z8[q][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int sp = 0; sp < a.z_splits; ++sp) {
+#pragma unroll
+    for (int q = 0; q < NZ; ++q) {
+      const int i = q * 64 * NWV + (int)threadIdx.x, row = i / bc;
+      if (i >= BM * bc || row0 + row >= a.T) continue;
+      const float* const from = a.z + ((int64_t)sp * a.T + row0 + row) * r + 8 * (i - row * bc);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) z8[q][p] += *reinterpret_cast<const f32x4*>(from + 4 * p);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NZ; ++q) {
+    const int i = q * 64 * NWV + (int)threadIdx.x, row = i / bc, c = i - row * bc;
+    if (i >= BM * bc) continue;
     u32x4 high, low;
-    z_operands(a, row0 + row, 8 * c, high, low);
+    split_operands(z8[q][0], z8[q][1], high, low);
     *reinterpret_cast<u32x4*>(z_at(row, c)) = high;
     *reinterpret_cast<u32x4*>(z_at(row, bc + c)) = low;
   }
@@ -272,25 +292,23 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
     one = next(who);
     if (one >= 0) load(one, buf ^ 1);
     const uint16_t* const b0 = b_lds + buf * BN * bc * 8;
-    auto frag = [&](int j, int c) {
-      return *reinterpret_cast<const u32x4*>(b0 + b_chunk(wcol0 + j * 32 + fr, c) * 8);
+    // operands of 16 ranks: B's rows, and z's high and low parts (rank 8: the two halves of the wavefront hold
+    // high and low of the same ranks)
+    const int nc = r == 8 ? 1 : r / 16;
+    auto b_frag = [&](int j, int c) {
+      return *reinterpret_cast<const u32x4*>(b0 + b_chunk(wcol0 + j * 32 + fr, r == 8 ? 0 : 2 * c + fg) * 8);
+    };
+    auto z_frag = [&](int f, int c, int part) {
+      return *reinterpret_cast<const u32x4*>(z_at(wrow0 + f * 32 + fr, r == 8 ? fg : part * bc + 2 * c + fg));
     };
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       if (now[f] == 0u) continue;
-      const int row = wrow0 + f * 32 + fr;
-      // operands of z: high and low of 16 ranks (rank 8: the two halves of the wavefront hold high and low of
-      // the same ranks)
-      const int nz = r == 8 ? 1 : r / 8;
-      auto z_frag = [&](int c) {
-        return *reinterpret_cast<const u32x4*>(z_at(row, r == 8 ? fg : (c & 1) * bc + (c & ~1) + fg));
-      };
-      auto b_frag = [&](int j, int c) { return frag(j, r == 8 ? 0 : (c & ~1) + fg); };
-      bool plain = now[f] == 0xffffffffu;
+      bool plain = now[f] == 0xffffffffu;  // zeros of z keep the adapter off the tokens without it
       if (!plain) {
         u16x2 most = {0, 0};
 #pragma unroll 1
-        for (int c = 0; c < nz; c += 2)
+        for (int c = 0; c < nc; ++c)
 #pragma unroll
           for (int j = 0; j < FN; ++j) largest(most, b_frag(j, c));
         plain = all_finite(most);
@@ -298,10 +316,15 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
       if (plain) {
         const bool mine = (now[f] >> fr) & 1u;
 #pragma unroll 1
-        for (int c = 0; c < nz; ++c) {
-          const u32x4 z = mine ? z_frag(c) : u32x4{0u, 0u, 0u, 0u};
+        for (int c = 0; c < nc; ++c) {
+          const u32x4 zero = {0u, 0u, 0u, 0u};
+          const u32x4 high = mine ? z_frag(f, c, 0) : zero, low = mine && r > 8 ? z_frag(f, c, 1) : zero;
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[f][j] = mfma32(z, b_frag(j, c), acc[f][j]);
+          for (int j = 0; j < FN; ++j) {
+            const u32x4 b = b_frag(j, c);
+            acc[f][j] = mfma32(high, b, acc[f][j]);
+            acc[f][j] = mfma32(low, b, acc[f][j]);
+          }
         }
       } else {
 #pragma unroll
@@ -310,7 +333,10 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
 #pragma unroll
           for (int v = 0; v < 16; ++v) term[v] = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < nz; ++c) term = mfma32(z_frag(c), b_frag(j, c), term);
+          for (int c = 0; c < nc; ++c) {
+            term = mfma32(z_frag(f, c, 0), b_frag(j, c), term);
+            if (r > 8) term = mfma32(z_frag(f, c, 1), b_frag(j, c), term);
+          }
           add_term(acc[f][j], term, now[f], fg);
         }
       }
