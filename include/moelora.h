@@ -425,7 +425,7 @@ int moe_lora_linear_lora(const void *x, const void *W, const float *w_scale, con
 #define MOELORA_GATE_SIGMOID 2  /* 1 / (1 + e^-g), g f32 [T] */
 #define MOELORA_GATE_FEATURES 3 /* g bf16 [T] rows of hidden; gate_stride 0: one row for every token */
 typedef struct {
-  int32_t T, hidden; /* T in [0, 2^30); hidden in [1, 32768] */
+  int32_t T, hidden; /* T in [0, 2^22); hidden in [1, 32768] */
   int32_t norm;      /* MOELORA_NORM_* */
   int32_t gate;      /* MOELORA_GATE_* */
   float eps;         /* finite, not negative */

@@ -1,7 +1,6 @@
 // C ABI of the operators of the block around the layer: the projection with a batch's adapters
 // (moe_lora_linear_lora), the norms (moe_lora_block_norm), and the layer for a few tokens
-// (moe_lora_forward_few), declared in include/moelora.h. Argument
-// checks and launches.
+// (moe_lora_forward_few), declared in include/moelora.h. Argument checks and launches.
 #include <algorithm>
 #include <cmath>
 
@@ -70,6 +69,7 @@ int validate_few(const moe_lora_dims* d, int32_t topk) {
   if (topk < 1 || topk > d->n_experts || topk > kMaxTopk) return MOELORA_EINVAL_DIMS;
   // 32-bit byte offsets: one expert's W1, one adapter's A1 of an expert, x, the activations
   const int64_t h = d->hidden, I = d->inter, most = (int64_t)1 << 31;
+  if (I >= most / 4 || h >= most / 4) return MOELORA_EINVAL_DIMS;
   if (4 * I * h >= most || 2 * d->rank * h >= most || 2 * kFewTokens * h >= most ||
       4 * (int64_t)kFewTokens * kMaxTopk * I >= most)
     return MOELORA_EINVAL_DIMS;
@@ -252,7 +252,8 @@ int moe_lora_block_norm(const void* y, const void* residual, const void* gate, c
                         const void* post_bias, const void* weight, const void* bias,
                         const moe_lora_block_norm_dims* d, void* sum, void* out, void* stream) {
   if (!d) return MOELORA_ENULL;
-  if (d->T < 0 || d->T >= (1 << 30) || d->hidden < 1 || d->hidden > kMaxNormHidden) return MOELORA_EINVAL_DIMS;
+  // (a launch holds 2^32 threads, of which the longest rows take 1024 each)
+  if (d->T < 0 || d->T >= (1 << 22) || d->hidden < 1 || d->hidden > kMaxNormHidden) return MOELORA_EINVAL_DIMS;
   if (d->norm != MOELORA_NORM_RMS && d->norm != MOELORA_NORM_LAYER) return MOELORA_EINVAL_DIMS;
   if (d->gate < MOELORA_GATE_NONE || d->gate > MOELORA_GATE_FEATURES) return MOELORA_EINVAL_DIMS;
   if (!std::isfinite(d->eps) || d->eps < 0.f || !std::isfinite(d->residual_scale) || !std::isfinite(d->branch_scale))
