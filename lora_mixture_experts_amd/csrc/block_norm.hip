@@ -8,19 +8,34 @@
 //
 // Bound by bytes: a row is read once and stays in registers as fp32, through both norms (the second one
 // takes s before its rounding), and each output is rounded once. Sums are fp32, of the deviations from the
-// mean where there is one.
+// mean where there is one. 16384 x 4096 with the branch's norm: 95.6 us, 5.6 TB/s, above what a copy reaches.
+// Few rows are latency: one of 4096 takes 3.3 us; 1531 of 2043, LayerNorm twice (four sums behind each other),
+// 9.8 us, 10.6 with the sums over a wavefront through LDS in place of DPP. Everything a row needs is loaded
+// before the first sum: where the residual and the weights came after the sums before them, 16384 x 4096 took
+// 96.5 us and the odd rows 10.1.
 #include "common.h"
 #include "kernels.h"
 #include "linear.h"
 
 namespace moelora {
 
+// The value of another lane, 0 for lanes without one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float from_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xf, false));
+}
+
 // Sum over the TPR threads of a row, in a fixed order. `buf`: the row's part of LDS, the two halves taken in
 // turn, so that one barrier a sum is enough.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  v += from_lane<0x111, 0xf>(v);  // (lanes 1, 2, 4, 8 before in a row of 16, then the rows before: lane 63 has all)
+  v += from_lane<0x112, 0xf>(v);
+  v += from_lane<0x114, 0xf>(v);
+  v += from_lane<0x118, 0xf>(v);
+  v += from_lane<0x142, 0xa>(v);
+  v += from_lane<0x143, 0xc>(v);
+  v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
   if (TPR == 64) return v;
   constexpr int W = TPR / 64;
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
@@ -31,22 +46,38 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
   return s;
 }
 
-// Eight elements of a row (zeros past its end).
-struct Eight {
-  float v[8];
+// Eight elements of a row as they are stored (zeros past its end). The lane at the end of a row loads the row's
+// last eight and, when it uses them, shifts out those of the lane before it (which may have stored its results
+// there: an output in place of an input). Element by element, its wavefront waited for each operand in turn.
+struct Raw {
+  u32x4 w;
   __device__ __forceinline__ void load(const uint16_t* p, int c, int h) {
-    if (c + 8 <= h) {
-      const u32x4 w = *reinterpret_cast<const u32x4_any*>(p + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-      }
+    if (h >= 8) {
+      w = *reinterpret_cast<const u32x4_any*>(p + min(c, h - 8));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < h ? bf16_to_f32(p[c + i]) : 0.f;
+      for (int i = 0; i < 4; ++i)
+        w[i] = (2 * i < h ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < h ? (uint32_t)p[2 * i + 1] << 16 : 0u);
     }
   }
+  __device__ __forceinline__ void get(float (&v)[8], int c, int h) const {
+    u32x4 x = w;
+    if (c + 8 > h && h >= 8) {
+      const int s = c + 8 - h;
+      if (s & 4) x = u32x4{x[2], x[3], 0u, 0u};
+      if (s & 2) x = u32x4{x[1], x[2], x[3], 0u};
+      if (s & 1) x = u32x4{x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(x[i]);
+      v[2 * i + 1] = bf16_hi(x[i]);
+    }
+  }
+};
+
+struct Eight {
+  float v[8];
   __device__ __forceinline__ void store(uint16_t* p, int c, int h) const {
     if (c + 8 <= h) {
       u32x4 w;
@@ -74,8 +105,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
   int turn = 0;
   auto sum = [&](float v) { return row_sum<TPR>(v, s_red[turn ^= 1]); };
   auto col = [&](int j) { return (j * TPR + lane) * 8; };
+  // Every load goes out before the first sum waits for one (the longest rows' weights and biases have no registers
+  // to wait in).
+  constexpr bool AHEAD = V <= 2;
+  struct {
+    Raw y[V], residual[V], gate[V], weight[V], bias[V], post_weight[V], post_bias[V];
+  } in;
+  auto load = [&](Raw (&to)[V], const uint16_t* p) {
+    if (!p) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (col(j) < h) to[j].load(p, col(j), h);
+  };
+  load(in.y, a.y ? a.y + t * a.ldy : nullptr);
+  load(in.residual, a.residual + t * a.ldr);
+  load(in.gate, a.gate ? a.gate + t * a.ldg : nullptr);
+  const float given = a.token_gate ? a.token_gate[t] : 0.f;
+  if constexpr (AHEAD) {
+    load(in.post_weight, a.post_weight);
+    load(in.post_bias, a.post_bias);
+    load(in.weight, a.weight);
+    load(in.bias, a.bias);
+  }
+  __builtin_amdgcn_sched_barrier(0);
   // (elements past the row's end: 0 in every sum, and never stored)
-  auto norm = [&](Eight (&x)[V], const uint16_t* w, const uint16_t* b) {
+  auto norm = [&](Eight (&x)[V], Raw (&w)[V], const uint16_t* from_w, Raw (&b)[V], const uint16_t* from_b) {
     float shift = 0.f, sq = 0.f;
     if (a.layer) {
       float s = 0.f;
@@ -97,11 +151,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (col(j) >= h) continue;
-      Eight wv, bv;
-      wv.load(w, col(j), h);
-      if (b) bv.load(b, col(j), h);
+      if constexpr (!AHEAD) {
+        w[j].load(from_w, col(j), h);
+        if (from_b) b[j].load(from_b, col(j), h);
+      }
+      float wv[8], bv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      w[j].get(wv, col(j), h);
+      if (from_b) b[j].get(bv, col(j), h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j].v[i] = x[j].v[i] * scale * wv.v[i] + (b ? bv.v[i] : 0.f);
+      for (int i = 0; i < 8; ++i) x[j].v[i] = x[j].v[i] * scale * wv[i] + bv[i];
     }
   };
 
@@ -113,29 +171,26 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
   if (a.y) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (col(j) < h) x[j].load(a.y + t * a.ldy, col(j), h);
-    if (a.post_weight) norm(x, a.post_weight, a.post_bias);
+      if (col(j) < h) in.y[j].get(x[j].v, col(j), h);
+    if (a.post_weight) norm(x, in.post_weight, a.post_weight, in.post_bias, a.post_bias);
   }
   float g = a.branch_scale;
-  if (a.token_gate) {
-    const float v = a.token_gate[t];
-    g *= a.sigmoid ? 1.f / (1.f + __expf(-v)) : v;
-  }
+  if (a.token_gate) g *= a.sigmoid ? 1.f / (1.f + __expf(-given)) : given;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     if (col(j) >= h) continue;
-    Eight res, gate;
-    res.load(a.residual + t * a.ldr, col(j), h);
-    if (a.gate) gate.load(a.gate + t * a.ldg, col(j), h);
+    float res[8], gate[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    in.residual[j].get(res, col(j), h);
+    if (a.gate) in.gate[j].get(gate, col(j), h);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float branch = a.y ? (a.gate ? g * gate.v[i] : g) * x[j].v[i] : 0.f;
-      x[j].v[i] = a.residual_scale * res.v[i] + branch;
+      const float branch = a.y ? g * gate[i] * x[j].v[i] : 0.f;
+      x[j].v[i] = a.residual_scale * res[i] + branch;
     }
     if (a.sum) x[j].store(a.sum + t * a.lds, col(j), h);
   }
   if (!a.weight) return;
-  norm(x, a.weight, a.bias);
+  norm(x, in.weight, a.weight, in.bias, a.bias);
 #pragma unroll
   for (int j = 0; j < V; ++j)
     if (col(j) < h) x[j].store(a.out + t * a.ldo, col(j), h);
