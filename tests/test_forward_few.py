@@ -105,6 +105,8 @@ SHAPES = [
     (3, 2048, 128, 16, 2, 7, 16), (5, 128, 1408, 6, 3, 9, 8), (7, 640, 640, 300, 4, 2, 32), (8, 256, 512, 8, 8, 8, 16),
     (13, 512, 384, 17, 16, 3, 8), (16, 256, 256, 32, 8, 16, 32), (16, 1152, 896, 4, 2, 5, 64), (16, 128, 128, 1024, 16, 2, 16),
     (16, 4096, 2048, 16, 2, 2, 16),
+    # every token on the same experts, mostly with adapters of their own
+    (16, 128, 128, 1, 1, 1, 8), (16, 4096, 256, 1, 1, 40, 16), (15, 2048, 384, 2, 2, 33, 64), (9, 4096, 11008, 1, 1, 16, 32),
 ]
 
 

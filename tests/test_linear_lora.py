@@ -113,6 +113,30 @@ def test_linear_lora_matches_float64(T, K, N, r, nA, pattern, act, w):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,nA,pattern", [
+    (511, 528, 96, 16, 600, "random"), (512, 1024, 200, 32, 1024, "distinct"), (512, 1040, 64, 8, 1, "one"),  # by adapter
+    (513, 528, 96, 16, 600, "random"), (300, 640, 96, 64, 1025, "random"), (33, 2048, 64, 16, 5000, "distinct"),  # by token
+    (2100, 272, 300, 64, 50, "random"), (3000, 2064, 70, 32, 31, "runs"), (3, 16384, 33, 64, 2, "random"),
+])
+def test_linear_lora_shrink_forms(T, K, N, r, nA, pattern):
+    """Both forms of the shrink on both sides of their borders, with K split and whole."""
+    _check(T, K, N, "none", "bf16", r, nA, pattern)
+
+
+@pytest.mark.gpu
+def test_linear_lora_rows_far_apart():
+    """Rows of x that lie 2^22 - 8 elements apart: offsets past 32 bits within a batch."""
+    T, K, N = 300, 256, 64
+    x, W, _, _, _ = _inputs(T, K, N, "none", "bf16", 91)
+    A, B = _adapters(20, 16, K, N, 91)
+    ids = _ids(T, 20, "random")
+    wide = torch.empty(T, (1 << 22) - 8, dtype=BF, device=DEV)
+    wide[:, 8:8 + K] = x
+    y = ml.linear_lora(wide[:, 8:8 + K], W, A, B, ids)
+    _compare(y, x, W, None, None, "none", None, A, B, ids)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act,w", [("gelu", "bf16"), ("swiglu", "bf16"), ("silu", "e4m3"), ("swiglu", "e4m3")])
 @pytest.mark.parametrize("form", range(len(FORMS)))
 def test_linear_lora_every_form(form, act, w):
