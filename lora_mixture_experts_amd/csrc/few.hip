@@ -314,7 +314,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_gate_up_kernel(FewArgs 
 
   f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   const int column = min(m, M - 1);  // (a product's columns are the members; columns past them are not read)
-  auto compute = [&](const Set& s, int step) {  // of the steps in LDS (one past them: its weights are zeros)
+  auto compute = [&](const Set& s, int step) {  // of the steps in LDS (past K: zeros)
     const int row = step * M + column;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_gate_up_kernel(FewArgs 
       }
       load(set[(q + NS - 1) % NS], i + q + NS - 1);
       __builtin_amdgcn_sched_barrier(0);
-      compute(set[q], min(i + q - begin, phase - 1) * KW + wk);
+      if (i + q < n) compute(set[q], (i + q - begin) * KW + wk);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
     if (i < i1 && (i == i1 - 1 || i - u * nch == nch - 1)) {  // this wavefront's last step of the expert
       const int kf = FT == 8 ? kq & 1 : kq;  // features 4 kf ..
       f32x4 scale = {1.f, 1.f, 1.f, 1.f};
-      if (W8) scale = *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)s_expert[u] * h + n0 + 4 * kf);
+      if (W8) scale = *reinterpret_cast<const f32x4_any*>(a.s2 + (int64_t)s_expert[u] * h + n0 + 4 * kf);
 #pragma unroll
       for (int p = 0; p < NA; ++p) {
         const int c = FT == 8 ? m & 3 : (m & 7) + 8 * p;
