@@ -49,6 +49,17 @@ ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
   return p;
 }
 
+// One token in one launch, where the streaming kernel takes it and forming z in every workgroup costs less than the
+// launch that it saves (some 4 us): its loads of A are K r a round of 256 workgroups. Two launches against one
+// (us), by that number: 16384 (1024 x 1024, rank 16) 7.2, 4.4; 65536 (4096 x 4096, rank 16) 12.1, 10.8; (1024 x
+// 1024, rank 64) 11.2, 7.7; (8192 x 1024 E4M3, rank 8) 11.2, 11.8; 131072 (4096 x 4096, rank 32) 13.2, 14.4; (2048
+// x 2048, rank 64) 12.6, 12.5; (8192 x 1024 E4M3, rank 16) 11.6, 14.8.
+bool one_launch(const moe_lora_linear_lora_dims* d, const LinearPlan& p) {
+  const moe_lora_linear_dims& l = d->linear;
+  const int64_t rounds = ((int64_t)l.out_features + 4095) / 4096;  // of workgroups, 16 columns each
+  return p.stream && l.T == 1 && rounds * l.in_features * d->rank <= 65536;
+}
+
 LoraLayout lora_layout(const moe_lora_linear_lora_dims* d, const LinearPlan& p) {
   const size_t T = (size_t)d->linear.T;
   LoraLayout L;
@@ -236,8 +247,6 @@ int moe_lora_linear_lora(const void* x, const void* W, const float* w_scale, con
   const ShrinkPlan sp = plan_shrink(d);
   sh.slots = sp.slots;
   sh.splits = sp.splits;
-  if (launch_token_shrink(sh, stream) != hipSuccess) return MOELORA_EHIP;
-
   LinearArgs a = linear_args(x, W, w_scale, bias, residual, &l, y, ws + L.part);
   a.z = sh.z;
   a.z_splits = sp.splits;
@@ -245,6 +254,8 @@ int moe_lora_linear_lora(const void* x, const void* W, const float* w_scale, con
   a.groups = sh.groups;
   a.flags = (int*)ws;
   a.r = d->rank;
+  if (one_launch(d, p)) return launch_linear_lora_one(a, sh, stream) == hipSuccess ? MOELORA_OK : MOELORA_EHIP;
+  if (launch_token_shrink(sh, stream) != hipSuccess) return MOELORA_EHIP;
   return launch_linear_lora(p, a, stream) == hipSuccess ? MOELORA_OK : MOELORA_EHIP;
 }
 

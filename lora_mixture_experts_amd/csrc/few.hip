@@ -148,12 +148,6 @@ __global__ __launch_bounds__(64 * kShrinkWaves, 4) void few_shrink_kernel(FewArg
   }
 }
 
-// Eight bf16 by eight floats.
-__device__ __forceinline__ float dot8(u32x4 w, const float* x) {
-  return x[0] * bf16_lo(w.x) + x[1] * bf16_hi(w.x) + x[2] * bf16_lo(w.y) + x[3] * bf16_hi(w.y) + x[4] * bf16_lo(w.z) +
-         x[5] * bf16_hi(w.z) + x[6] * bf16_lo(w.w) + x[7] * bf16_hi(w.w);
-}
-
 // k of a lane's operand j of a 128-wide step. bf16: a load covers 64 contiguous bytes of each row; E4M3: 16
 // codes, which serve two operands, lie side by side.
 template <bool W8>

@@ -313,6 +313,7 @@ hipError_t launch_linear_tiled(const LinearPlan& p, LinearArgs a, hipStream_t st
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
 hipError_t launch_few(const FewArgs& a, int col_tiles, hipStream_t stream);
 hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream);
+hipError_t launch_linear_lora_one(const LinearArgs& a, const TokenShrinkArgs& sh, hipStream_t stream);
 hipError_t launch_linear_lora(const LinearPlan& p, const LinearArgs& a, hipStream_t stream);
 hipError_t launch_sgmv_expand(const SgmvArgs& a, int max_blocks, hipStream_t stream);
 // D parts: d_parts == nullptr: ksplit parts for every row; else d_parts[(row / part_rows) *

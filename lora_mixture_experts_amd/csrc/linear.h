@@ -169,6 +169,12 @@ __device__ __forceinline__ void z_operands(const LinearArgs& a, int t, int q, u3
   split_operands(v[0], v[1], high, low);
 }
 
+// Eight bf16 by eight floats.
+__device__ __forceinline__ float dot8(u32x4 w, const float* x) {
+  return x[0] * bf16_lo(w.x) + x[1] * bf16_hi(w.x) + x[2] * bf16_lo(w.y) + x[3] * bf16_hi(w.y) + x[4] * bf16_lo(w.z) +
+         x[5] * bf16_hi(w.z) + x[6] * bf16_lo(w.w) + x[7] * bf16_hi(w.w);
+}
+
 // The flag of moe_lora_debug_status for a call with adapters: one wavefront, once every group is written.
 __device__ __forceinline__ void report_adapter_range(const LinearArgs& a) {
   bool bad = false;
