@@ -187,10 +187,13 @@ struct AdapterRows {
 // after another, straight into one of two buffers while the adapter before is multiplied. 16-byte chunks,
 // XOR-swizzled by the row so that fragment reads are free of bank conflicts. (With B in registers as above the
 // accumulators spilled: 4096 x 28672 x 4096, rank 64, 1.60 ms.) wrow_of(i): B's row of row i of the weight tile,
-// -1 past the end. Every wavefront of the workgroup calls it.
+// -1 past the end; groups: the adapters of the tile's rows, in LDS (loaded beside the main loop's first tiles: a
+// load behind the main loop is the longer the more the other workgroups load). Every wavefront of the workgroup
+// calls it.
 template <int BM, int BN, int NWV, int FM, int FN, class Row>
 __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const LinearArgs& a, int row0, int wrow0, int wcol0,
-                                                  Row wrow_of, uint16_t* lds, int part, int parts, int wave, int lane) {
+                                                  Row wrow_of, uint16_t* lds, const TokenAdapters* groups, int part, int parts,
+                                                  int wave, int lane) {
   static_assert(BM == 256 && BN % 256 == 0, "four groups of 32 tokens in two halves of a wavefront");
   constexpr int NG = BM / 64;  // registers that hold the adapters of the tile's BM / 32 groups, 32 lanes each
   const int fr = lane & 31, fg = lane >> 5, r = a.r;
@@ -204,17 +207,10 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
   uint64_t left[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
-    const int t = row0 + 64 * i + 32 * fg;
-    adapter[i] = -1;
-    tokens[i] = 0u;
-    bool in = false;
-    if (t < a.T) {
-      const TokenAdapters& g = a.groups[t >> 5];
-      in = fr < g.n;
-      adapter[i] = g.adapter[fr];
-      tokens[i] = g.tokens[fr];
-    }
-    left[i] = __ballot(in);
+    const TokenAdapters& g = groups[2 * i + fg];
+    adapter[i] = g.adapter[fr];
+    tokens[i] = g.tokens[fr];
+    left[i] = __ballot(fr < g.n);
   }
   uint32_t who[FM];  // tokens of this wavefront's fragments that carry the adapter
   int turn = 0;
@@ -345,6 +341,13 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
   }
 }
 
+// LDS of the stages, or of the epilogue's regions; bytes of the adapters of a tile's rows behind it, in whole
+// wavefronts' loads.
+template <class Pipe, int NWV, int KG, int WN>
+constexpr int kTiledLds = KG * (Pipe::LDS_BYTES > NWV * 32 * WN * 4 ? Pipe::LDS_BYTES : NWV * 32 * WN * 4);
+template <int BM>
+constexpr int kTileGroups = (BM / 32 * (int)sizeof(TokenAdapters) + 1023) / 1024 * 1024;
+
 template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8, bool STREAM = false,
           bool LORA = false>
 __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_tiled_kernel(LinearArgs a) {
@@ -355,6 +358,8 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
   constexpr int WB = W8 ? 1 : 2;
   static_assert(!GATED || FN % 2 == 0, "gate and up halves in each wavefront");
   static_assert(!GATED || (WN / 2) % Pipe::RPBB == 0, "a load block is all gate or all up rows");
+  // behind the stages, the epilogue's regions and z with B: the adapters of the tile's rows
+  [[maybe_unused]] constexpr int GROUPS_AT = kTiledLds<Pipe, NWV, KG, WN>;
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -461,6 +466,12 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   Pipe::run_steps(acc, ld, lds + kg * (Pipe::LDS_BYTES / 2), nsteps, wave, lane, [&] {
     if constexpr (LORA && FM == 1) rows_ad.load_first(a, part, parts);
+    if constexpr (LORA && FM > 1) {  // (groups past the last one: zeros, no adapter)
+      const int g0 = row0 / 32, have = min(BM / 32, (a.T + 31) / 32 - g0);
+      const u32x4 gr = buffer_desc(a.groups + g0, (uint32_t)(have * sizeof(TokenAdapters)));
+      for (int i = wave; i * 1024 < kTileGroups<BM>; i += NWV)
+        lds_dma16(gr, (uint32_t)(i * 1024 + lane * 16), 0u, (uint32_t)(uintptr_t)lds + GROUPS_AT + i * 1024);
+    }
   });
 
   if constexpr (LORA) {  // (the adapters' term takes no weight scale)
@@ -473,7 +484,9 @@ __global__ __launch_bounds__(64 * KG * (BM / WM) * (BN / WN), 1) void linear_til
           for (int v = 0; v < 16; ++v) acc[i][j][v] *= sc[j];
     }
     if constexpr (FM == 1) rows_ad.add(acc[0], a, row0 + wm * WM, part, parts, lane);
-    else add_adapters_tile<BM, BN, NWV, FM, FN>(acc, a, row0, wm * WM, wn * WN, wrow_of, lds, part, parts, wave, lane);
+    else add_adapters_tile<BM, BN, NWV, FM, FN>(acc, a, row0, wm * WM, wn * WN, wrow_of, lds,
+                                                       reinterpret_cast<const TokenAdapters*>(lds + GROUPS_AT / 2), part,
+                                                       parts, wave, lane);
 #pragma unroll
     for (int j = 0; j < FN; ++j) sc[j] = 1.f;
     if (tk == 0 && wave_all == NWV * KG - 1) report_adapter_range(a);
@@ -614,11 +627,11 @@ namespace {
 template <int BM, int BN, int WM, int WN, int NST, int KG, bool GATED, bool W8, bool LORA, bool STREAM = false>
 hipError_t launch_tile(LinearArgs a, hipStream_t stream) {
   constexpr int NWV = (BM / WM) * (BN / WN);
-  constexpr int ring = KG * TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>::LDS_BYTES;
-  constexpr int out = KG * NWV * 32 * WN * 4;  // the epilogue's regions
-  constexpr int bytes = ring > out ? ring : out;
+  constexpr int base = kTiledLds<TilePipe<BM, BN, WM, WN, 64, NST, false, NWV, W8>, NWV, KG, WN>;
+  constexpr bool behind = LORA && WM > 32;  // the adapters' term goes through LDS behind the main loop
+  constexpr int bytes = base + (behind ? kTileGroups<BM> : 0);
   static_assert(bytes <= kLdsBytes, "LDS stages must fit");
-  static_assert(WM == 32 || BM * 256 + 2 * BN * 128 <= bytes, "z and two adapters' rows of B of rank 64 must fit");
+  static_assert(!behind || (KG == 1 && BM * 256 + 2 * BN * 128 <= base), "z and two adapters' rows of B of rank 64 must fit");
   auto kern = linear_tiled_kernel<BM, BN, WM, WN, NST, KG, GATED, W8, STREAM, LORA>;
   static bool attr_set[64] = {};
   int dev = 0;
