@@ -410,6 +410,7 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
     int n = 0, flags = 0;
     for (int i = 0; i < P; i += 64) {
       const int p = i + lane, tokens = p < P ? a.members[p] : 0, entries = (tokens + C - 1) / C;
+      const int e = p < P ? a.ids[p] : -1;
       if (p < P) flags |= a.pair_flags[p];
       int before = 0, all = 0;  // entries of the lanes before, and of all
 #pragma unroll
@@ -421,6 +422,7 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
       for (int q = 0; q < entries; ++q) {
         s_lead[n + before + q] = p * kFewTokens + q * C;
         s_m[n + before + q] = (uint8_t)min(tokens - q * C, C);
+        s_expert[n + before + q] = e;
       }
       n += all;
     }
@@ -436,21 +438,17 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
   }
   __syncthreads();
   const int U = s_n;
-  for (int i = tid; i < U * C; i += NTH) {
+  // (the first columns' before the weights, which take longer, the others behind them)
+  auto column = [&](int i, int& pair, float& w) {
     const int u = i / C, c = i % C;
-    const bool in = c < s_m[u];
-    s_pair[i] = in ? (int16_t)a.member_pair[s_lead[u] + c] : (int16_t)-1;
-    s_wt[i] = in ? a.member_w[s_lead[u] + c] : 0.f;
-    if (c == 0) s_expert[u] = s_ids[s_lead[u] / kFewTokens];
-  }
-  for (int p = tid; p < P; p += NTH) {  // the token's first pair with the expert holds z2's parts
-    int first = p;
-    for (int q = p - 1; q >= p / k * k; --q)
-      if (s_ids[q] == s_ids[p]) first = q;
-    s_first[p] = first;
-  }
-  __syncthreads();
-
+    const bool in = i < U * C && c < s_m[u];
+    pair = in ? a.member_pair[s_lead[u] + c] : -1;
+    w = in ? a.member_w[s_lead[u] + c] : 0.f;
+  };
+  int pair0;
+  float w0;
+  column(min(tid, MAXP * C - 1), pair0, w0);
+  __builtin_amdgcn_sched_barrier(0);
   // Steps i0 .. i1 - 1 of this wavefront: entry i / nch, K step i % nch.
   const int nk = K / 128, nch = (nk + SUB - 1) / SUB, total = U * nch;
   const int i0 = (int)((int64_t)total * wave / NW), i1 = (int)((int64_t)total * (wave + 1) / NW);
@@ -472,6 +470,19 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
   Set set[NS];
 #pragma unroll
   for (int q = 0; q < NS - 1; ++q) load(set[q], i0 + q);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int i = tid; i < U * C; i += NTH) {
+    if (i != tid) column(i, pair0, w0);
+    s_pair[i] = (int16_t)pair0;
+    s_wt[i] = w0;
+  }
+  for (int p = tid; p < P; p += NTH) {  // the token's first pair with the expert holds z2's parts
+    int first = p;
+    for (int q = p - 1; q >= p / k * k; --q)
+      if (s_ids[q] == s_ids[p]) first = q;
+    s_first[p] = first;
+  }
+  __syncthreads();
   // A block: the steps from i on, of one entry, whose act fits the region.
   auto block_steps = [&](int i) {
     const int u = i / nch;
