@@ -374,19 +374,18 @@ __global__ __launch_bounds__(64 * kFewWaves, 4) void few_gate_up_kernel(FewArgs 
 // them, and add an expert's sums, weighted, to its tokens' (in LDS, a place for each wavefront) at its last step
 // there. Before, behind their first weight loads, they form the adapters' term: z2 from its parts, in tile
 // order, and z2 B2^T.
-// FT = 16: a step is 128 of K; the columns of a product are the high parts of 8 tokens' act and their low parts,
-// NA products a step. FT = 8, where 16 would leave CUs without a workgroup: a step is 256 of K, whose halves
+// FT = 16: a step is 128 of K; the columns of a product are the high parts of 8 tokens' act and their low parts.
+// FT = 8, where 16 would leave CUs without a workgroup: a step is 256 of K, whose halves
 // are rows 0 .. 7 and 8 .. 15 of a product and have columns of their own (high and low parts of 4 tokens), so that
 // a load still brings 1 KB. An expert of more tokens than a step has columns for comes several times.
 // act passes through LDS, a region for each wavefront: as many steps at once as the expert's tokens leave room
 // for, so that act costs as few load instructions as its bytes need (a load costs a CU some 50 cycles whatever it
 // brings; an operand a load, as the weights come, doubled their number: 16 tokens, 8 of 128 experts, 135 us).
-template <int FT, int NA, bool W8>
-__global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(FewArgs a) {
-  constexpr int NW = kFewDownWaves / NA, NTH = 64 * NW, MAXP = kFewTokens * kMaxTopk;
-  constexpr int SUB = FT == 8 ? 2 : 1, C = FT == 8 ? 4 : 8 * NA;  // 128-wide parts of a step; columns of a step
-  static_assert(FT == 16 || NA == 1, "one product of 4 tokens in 8 features' steps");
-  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = W8 ? 6 : 3, AL = 4 * NA;  // act loads of a block
+template <int FT, bool W8>
+__global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a) {
+  constexpr int NW = kFewDownWaves, NTH = 64 * NW, MAXP = kFewTokens * kMaxTopk;
+  constexpr int SUB = FT == 8 ? 2 : 1, C = FT == 8 ? 4 : 8;  // 128-wide parts of a step; tokens of a step
+  constexpr int WL = W8 ? 2 : 4, WB = W8 ? 1 : 2, NS = W8 ? 6 : 3, AL = 4;  // act loads of a block
   // entries: experts, those of many tokens several times; place of its tokens among the members, expert, tokens
   __shared__ int s_ids[MAXP], s_first[MAXP], s_ad[kFewTokens], s_lead[MAXP], s_expert[MAXP], s_n;
   __shared__ uint8_t s_m[MAXP];
@@ -556,9 +555,7 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  f32x4 acc[NA];
-#pragma unroll
-  for (int p = 0; p < NA; ++p) acc[p] = zero;
+  f32x4 acc = zero;
   uint8_t* const own = s_act[wave];
   int begin = 0, end = i0, M = 1;  // the block in LDS, its entry's tokens
   auto compute = [&](const Set& s, int i) {
@@ -582,36 +579,30 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const u32x4 wv = W8 ? e4m3x8_to_bf16(s.w[j / 2 % WL], j % 2) : s.w[j % WL];
-#pragma unroll
-      for (int p = 0; p < NA; ++p) {
-        const int c = FT == 8 ? m & 3 : (m & 7) + 8 * p, part = FT == 8 ? (m >> 2) & 1 : m >> 3;
-        const int row = (g * M + min(c, M - 1)) * 2 + part, chunk = few_k<W8>(j, kq) / 8;
-        acc[p] = mfma16(wv, *reinterpret_cast<const u32x4*>(own + row * 256 + (chunk ^ (row & 15)) * 16), acc[p]);
-      }
+      const int c = FT == 8 ? m & 3 : m & 7, part = FT == 8 ? (m >> 2) & 1 : m >> 3;
+      const int row = (g * M + min(c, M - 1)) * 2 + part, chunk = few_k<W8>(j, kq) / 8;
+      acc = mfma16(wv, *reinterpret_cast<const u32x4*>(own + row * 256 + (chunk ^ (row & 15)) * 16), acc);
     }
     const int u = i / nch;
     if (i < i1 && (i == i1 - 1 || i - u * nch == nch - 1)) {  // this wavefront's last step of the expert
       const int kf = FT == 8 ? kq & 1 : kq;  // features 4 kf ..
       f32x4 scale = {1.f, 1.f, 1.f, 1.f};
       if (W8) scale = *reinterpret_cast<const f32x4_any*>(a.s2 + (int64_t)s_expert[u] * h + n0 + 4 * kf);
+      const int c = FT == 8 ? m & 3 : m & 7;
+      const int pair = s_pair[u * C + c];
+      const float w = s_wt[u * C + c];
+      const bool mine = pair >= 0 && (FT == 8 ? kq < 2 && m < 4 : m < 8);
 #pragma unroll
-      for (int p = 0; p < NA; ++p) {
-        const int c = FT == 8 ? m & 3 : (m & 7) + 8 * p;
-        const int pair = s_pair[u * C + c];
-        const float w = s_wt[u * C + c];
-        const bool mine = pair >= 0 && (FT == 8 ? kq < 2 && m < 4 : m < 8);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          float v = acc[p][f];
-          if (FT == 8) {
-            v += __shfl_xor(v, 4);   // high and low
-            v += __shfl_xor(v, 40);  // the halves of the steps: rows and columns 8 further
-          } else {
-            v += __shfl_xor(v, 8);
-          }
-          if (mine) s_sum[wave][pair / k][4 * kf + f] += w * (v * scale[f]);
-          acc[p][f] = 0.f;
+      for (int f = 0; f < 4; ++f) {
+        float v = acc[f];
+        if (FT == 8) {
+          v += __shfl_xor(v, 4);   // high and low
+          v += __shfl_xor(v, 40);  // the halves of the steps: rows and columns 8 further
+        } else {
+          v += __shfl_xor(v, 8);
         }
+        if (mine) s_sum[wave][pair / k][4 * kf + f] += w * (v * scale[f]);
+        acc[f] = 0.f;
       }
     }
   };
@@ -638,11 +629,11 @@ __global__ __launch_bounds__(64 * (kFewDownWaves / NA)) void few_down_kernel(Few
 
 namespace {
 
-template <int FT, int NA>
+template <int FT>
 void launch_down(const FewArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.h / FT)), block(64 * (kFewDownWaves / NA));
-  if (a.s1) hipLaunchKernelGGL((few_down_kernel<FT, NA, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((few_down_kernel<FT, NA, false>), grid, block, 0, stream, a);
+  const dim3 grid((unsigned)(a.h / FT)), block(64 * kFewDownWaves);
+  if (a.s1) hipLaunchKernelGGL((few_down_kernel<FT, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((few_down_kernel<FT, false>), grid, block, 0, stream, a);
 }
 
 }  // namespace
@@ -671,11 +662,11 @@ hipError_t launch_few(const FewArgs& a, int ct, hipStream_t stream) {
 #undef MOELORA_FEW
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  // two products a step where experts have more than 4 tokens on average; 8 features a workgroup where 16 leave
-  // CUs without one, unless experts have more tokens than its steps have columns for
-  if (a.T > 8 && P > 4 * a.E) launch_down<16, 2>(a, stream);
-  else if (a.h / 16 < 256 && (a.T <= 4 || P <= 2 * a.E)) launch_down<8, 1>(a, stream);
-  else launch_down<16, 1>(a, stream);
+  // 8 features a workgroup where 16 leave CUs without one. Measured, 8 and 16 (us, the whole layer): 2048 features,
+  // 768 columns, 16 tokens, 8 of 128 experts 170, 192; 1024, 2048 columns, 12 tokens, 2 of 4 experts 38.5, 40.4;
+  // 2048, 5504 columns, 12 tokens, one expert 48.2, 47.0; 4096, 4096 columns, 16 tokens, 2 of 4 experts 152, 122.
+  if (a.h / 16 < 256) launch_down<8>(a, stream);
+  else launch_down<16>(a, stream);
   return hipGetLastError();
 }
 
