@@ -48,7 +48,8 @@ __device__ __forceinline__ int adapter_of(const TokenShrinkArgs& a, int t0, int 
 // Shrink of prompts: a workgroup takes 32 consecutive tokens and, of the distinct adapters among them, the ones of
 // index `slot`, + slots, ..: an adapter's rows of A are read once for all its tokens of the group (the tokens of a
 // prompt lie together, no sort is needed). Tokens without the adapter load zeros, which costs no traffic, and
-// their sums are dropped.
+// their sums are dropped. 4096 tokens of 4096, rank 64: 28 us, 1.2 TB/s of x: a load that touches 16 rows costs a CU
+// some 50 cycles whatever it brings.
 // NQ: 16-row tiles of A (rank 8 and 16: 1, 32: 2, 64: 4).
 template <int NQ>
 __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenShrinkArgs a) {
@@ -106,8 +107,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 }
 
 // Shrink of batches, whose tokens are mostly of different requests: a workgroup an adapter (blockIdx.y) and split
-// of K, which looks its tokens up among all ids, so that A is read once (by 32 tokens as above, 256 tokens of 64
-// adapters read it three times: 10.5 us). The workgroups behind the last adapter write the tokens' groups.
+// of K, which looks its tokens up among all ids, so that A is read once: 256 tokens of 4096, 64 adapters of rank 16,
+// 6.3 us (by 32 tokens as above, which reads it three times, 10.5). The workgroups behind the last adapter write the tokens' groups.
 template <int NQ>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(TokenShrinkArgs a) {
   constexpr int WK = kShrinkWaves;
