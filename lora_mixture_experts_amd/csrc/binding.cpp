@@ -1,7 +1,8 @@
 // Compiled half of the Python binding for the operators whose kernels take a few microseconds
-// (moe_lora_route, moe_lora_linear, moe_lora_linear_lora, moe_lora_block_norm, moe_lora_forward_few): checks of torch tensors, outputs and workspaces from torch's
-// allocator, torch's current stream, one call of the C ABI. As attribute reads and ctypes conversions in
-// Python the same took 6 us of a 10 us call; here 1 us.
+// (moe_lora_route, moe_lora_linear, moe_lora_linear_lora, moe_lora_block_norm, moe_lora_forward_few):
+// checks of torch tensors, outputs and workspaces from torch's allocator, torch's current stream, one call
+// of the C ABI. As attribute reads and ctypes conversions in Python the same took 6 us of a 10 us call;
+// here 1 us.
 //
 // Every function returns its output tensors, or the int code of a call that the C ABI refused.
 #include <Python.h>
