@@ -30,26 +30,28 @@ struct LoraLayout {
   size_t z, groups, part, total;
 };
 
-// The shrink's form: adapter by adapter (slots = 0) for batches of many requests, else 32 tokens after another, with
-// four workgroups for their adapters (prompts mostly have one). The first reads an adapter's A once, the second
-// once for every 32 tokens, but a workgroup of the first has all tokens of its adapter to itself. Measured, first
-// and second (us, 4096 x 1024, rank 16, random ids): 64 tokens of 4 adapters 16.7, 15.7; of 8 15.6, 17.4; 128 of 4
-// 18.7, 16.4; of 8 17.7, 18.1; of 32 17.0, 24.2; 512 of 8 28.6, 25.9; of 16 25.9, 32.1; of 64 24.4, 42.8.
+// The shrink's form: adapter by adapter (slots = 0) for batches, else 32 tokens after another, with four workgroups
+// for their adapters (prompts mostly have one). The first reads an adapter's A once for 16 of its tokens, the
+// second once for every 32 tokens. Measured, first and second (us, 4096 x 1024, rank 16, random ids): 64 tokens of 1
+// adapter 14.3, 14.7; of 8 15.7, 17.5; of 64 17.0, 26.7; 256 of 1 16.3, 16.7; of 64 20.7, 31.1; 512 of 2 23.1, 21.4; of
+// 16 24.8, 32.1; of 64 25.3, 42.7. The first form's parts share the tokens of one adapter, as far as 2048 workgroups go,
+// most of which find no token and leave (101 tokens of one of 43 adapters, 2792 x 660, rank 64: 38.2 with one part, 21.4
+// with 1024 workgroups, 19.6).
 // K is split (not below 512 of it) where that leaves CUs idle.
 struct ShrinkPlan {
-  int slots, splits;
+  int slots, splits, parts;
 };
 
 ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
   const moe_lora_linear_dims& l = d->linear;
   const int groups = std::max(1, (l.T + 31) / 32);
   ShrinkPlan p;
-  const bool batch = l.T <= kAdapterShrinkTokens && d->n_adapters > 4 && l.T <= 32 * (int64_t)d->n_adapters &&
-                     d->n_adapters <= 1024 && l.T * l.x_stride * 2 < ((int64_t)1 << 31);
+  const bool batch = l.T <= kAdapterShrinkTokens && d->n_adapters <= 1024 && l.T * l.x_stride * 2 < ((int64_t)1 << 31);
   p.slots = batch ? 0 : std::min({4, std::max(l.T, 1), d->n_adapters});
   const int busy = batch ? std::max(1, std::min(l.T, d->n_adapters)) : groups, enough = batch ? 257 : 128;
   p.splits = 1;
   while (p.splits < 8 && busy * p.splits < enough && l.in_features >= 1024 * p.splits) p.splits *= 2;
+  p.parts = batch ? std::max(1, std::min((l.T + 15) / 16, 2048 / (d->n_adapters * p.splits))) : 1;
   return p;
 }
 
@@ -253,6 +255,7 @@ int moe_lora_linear_lora(const void* x, const void* W, const float* w_scale, con
   const ShrinkPlan sp = plan_shrink(d);
   sh.slots = sp.slots;
   sh.splits = sp.splits;
+  sh.parts = sp.parts;
   LinearArgs a = linear_args(x, W, w_scale, bias, residual, &l, y, ws + L.part);
   a.z = sh.z;
   a.z_splits = sp.splits;

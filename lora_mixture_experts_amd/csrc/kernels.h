@@ -190,6 +190,7 @@ struct TokenShrinkArgs {
   TokenAdapters* groups;  // [ceil(T / 32)]
   int slots;   // workgroups that share the adapters of 32 tokens; 0: a workgroup an adapter
   int splits;  // workgroups that share K: 1, 2, 4 or 8
+  int parts;   // slots = 0: workgroups that share an adapter's tokens, 16 after 16
 };
 
 // Dense projection y = act(scale * (x W^T) + bias) + residual (moe_lora_linear), with adapters

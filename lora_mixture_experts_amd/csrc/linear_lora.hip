@@ -107,8 +107,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 }
 
 // Shrink of batches, whose tokens are mostly of different requests: a workgroup an adapter (blockIdx.y) and split
-// of K, which looks its tokens up among all ids, so that A is read once: 256 tokens of 4096, 64 adapters of rank 16,
-// 6.3 us (by 32 tokens as above, which reads it three times, 10.5). The workgroups behind the last adapter write the tokens' groups.
+// of K, which looks its tokens up among all ids, so that A is read once for 16 of them: 256 tokens of 4096, 64
+// adapters of rank 16, 6.3 us (by 32 tokens as above, which reads it three times, 10.5). The tokens of one adapter, 16
+// after 16, are shared by blockIdx.z. The workgroups behind the last adapter write the tokens' groups.
 template <int NQ>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(TokenShrinkArgs a) {
   constexpr int WK = kShrinkWaves;
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Token
   const int one = blockIdx.y, sp = blockIdx.x, K = a.K, r = a.r;
   if (one >= a.nA) {
     const int group = (one - a.nA) * WK + wk;
-    if (sp != 0 || group >= (a.T + 31) / 32) return;
+    if (sp != 0 || blockIdx.z != 0 || group >= (a.T + 31) / 32) return;
     bool bad;
     const int ad = adapter_of(a, group * 32, lane, bad);
     write_group(a, group, ad, bad);
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Token
     if (w < wk) before += s_n[w];
     n += s_n[w];
   }
-  if (n == 0) return;
+  if (n <= 16 * (int)blockIdx.z) return;
   if (mine) s_tok[before + (int)__popcll(all & lanemask_lt())] = tid;
   __syncthreads();
   const int chunks = (K + 63) / 64;
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Token
   uint32_t ao[NQ];
 #pragma unroll
   for (int c = 0; c < NQ; ++c) ao[c] = c * 16 + m < r ? (uint32_t)((size_t)(c * 16 + m) * K * 2) : kOutOfRange;
-  for (int i0 = 0; i0 < n; i0 += 16) {
+  for (int i0 = 16 * (int)blockIdx.z; i0 < n; i0 += 16 * (int)gridDim.z) {
     const int tok = i0 + m < n ? s_tok[i0 + m] : -1;
     const uint32_t xo[1] = {tok >= 0 ? (uint32_t)(tok * a.ldx * 2) : kOutOfRange};
     shrink_rows<NQ, 1>(part, ar, ao, xr, xo, k0, k1, wk, lane);
@@ -319,12 +320,13 @@ hipError_t launch_linear_lora_one(const LinearArgs& a, const TokenShrinkArgs& sh
 
 hipError_t launch_token_shrink(const TokenShrinkArgs& a, hipStream_t stream) {
   if (a.T <= 0) return hipSuccess;
-  if (a.slots < 0 || a.slots > 32 || a.splits < 1 || a.splits > 8 || a.K % 8 != 0) return hipErrorInvalidValue;
+  if (a.slots < 0 || a.slots > 32 || a.splits < 1 || a.splits > 8 || a.parts < 1 || a.K % 8 != 0) return hipErrorInvalidValue;
   const int groups = (a.T + 31) / 32;
   const dim3 block(64 * kShrinkWaves);
   if (a.slots == 0) {
     if (a.T > kAdapterShrinkTokens || (int64_t)a.T * a.ldx * 2 >= (int64_t)kOutOfRange) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)a.splits, (unsigned)(a.nA + (groups + kShrinkWaves - 1) / kShrinkWaves));
+    const dim3 grid((unsigned)a.splits, (unsigned)(a.nA + (groups + kShrinkWaves - 1) / kShrinkWaves),
+                    (unsigned)a.parts);
     if (a.r == 8 || a.r == 16) hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, block, 0, stream, a);
     else if (a.r == 32) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, block, 0, stream, a);
     else if (a.r == 64) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, block, 0, stream, a);

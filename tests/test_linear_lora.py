@@ -115,7 +115,7 @@ def test_linear_lora_matches_float64(T, K, N, r, nA, pattern, act, w):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,N,r,nA,pattern", [
     (511, 528, 96, 16, 600, "random"), (512, 1024, 200, 32, 1024, "distinct"), (160, 1040, 64, 8, 5, "random"),  # by adapter
-    (161, 1040, 64, 8, 5, "random"), (40, 512, 64, 16, 4, "random"), (512, 1040, 64, 8, 1, "one"),  # by token
+    (161, 1040, 64, 64, 5, "one"), (40, 512, 64, 16, 4, "random"), (512, 1040, 64, 8, 1, "one"), (511, 4096, 64, 64, 1000, "one"),
     (513, 528, 96, 16, 600, "random"), (300, 640, 96, 64, 1025, "random"), (33, 2048, 64, 16, 5000, "distinct"),  # by token
     (2100, 272, 300, 64, 50, "random"), (3000, 2064, 70, 32, 31, "runs"), (3, 16384, 33, 64, 2, "random"),
 ])
