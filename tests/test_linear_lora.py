@@ -125,6 +125,22 @@ def test_linear_lora_shrink_forms(T, K, N, r, nA, pattern):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(16, 1), (80, 17), (1008, 250), (1024, 1000), (4096, 48), (8192, 33), (8208, 16), (1024, 4112)])
+@pytest.mark.parametrize("r", [8, 16, 32, 64])
+@pytest.mark.parametrize("act,w", [("gelu", "bf16"), ("swiglu", "bf16"), ("none", "e4m3"), ("swiglu", "e4m3")])
+def test_linear_lora_one_token(K, N, r, act, w):
+    """In one launch and in two, with an adapter, without one, and beside an adapter of NaNs."""
+    for pattern in ("one", "none"):
+        _check(1, K, N, act, w, r, 3, pattern)
+    x, W, scale, _, _ = _inputs(1, K, N, act, w, 5, False, False)
+    A, B = _adapters(3, r, K, W.shape[0], 5)
+    ids = _ids(1, 2, "one")
+    y = ml.linear_lora(x, W, A, B, ids, w_scale=scale, act=act)
+    A[2], B[0] = math.nan, math.inf
+    assert torch.equal(y, ml.linear_lora(x, W, A, B, ids, w_scale=scale, act=act))
+
+
+@pytest.mark.gpu
 def test_linear_lora_rows_far_apart():
     """Rows of x that lie 2^22 - 8 elements apart: offsets past 32 bits within a batch."""
     T, K, N = 300, 256, 64
@@ -208,7 +224,7 @@ def test_linear_lora_broken_adapter_stays_with_its_tokens(T, N, pattern, bad):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
 def test_linear_lora_adapter_ids_out_of_range(T):
     """Taken as none, and told by the workspace's flags."""
     K, N, nA = 512, 96, 3
@@ -229,7 +245,7 @@ def test_linear_lora_adapter_ids_out_of_range(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,K,N", [(7, 512, 100), (40, 512, 100), (130, 512, 100), (520, 528, 203)])
+@pytest.mark.parametrize("T,K,N", [(1, 512, 100), (7, 512, 100), (40, 512, 100), (130, 512, 100), (520, 528, 203)])
 @pytest.mark.parametrize("act,w", [("none", "bf16"), ("swiglu", "bf16"), ("none", "e4m3")])
 def test_linear_lora_strided_rows(T, K, N, act, w):
     """x, W, residual and y inside wider buffers, whose other columns hold NaN and stay untouched."""
@@ -283,7 +299,7 @@ def test_linear_lora_poisoned_workspace_and_other_streams(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [8, 64, 200])
+@pytest.mark.parametrize("T", [1, 8, 64, 200])
 def test_linear_lora_graph_replays(T):
     """Captured with a workspace of its own; other adapters at every replay, eager calls between."""
     K, N = 2048, 192
