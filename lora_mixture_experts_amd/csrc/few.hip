@@ -597,12 +597,10 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         float v = acc[f];
-        if (FT == 8) {
-          v += __shfl_xor(v, 4);   // high and low
-          v += __shfl_xor(v, 40);  // the halves of the steps: rows and columns 8 further
-        } else {
-          v += __shfl_xor(v, 8);
-        }
+        const float low = __shfl_xor(v, FT == 8 ? 4 : 8);
+        // (an infinity of W2 is the high part's: times the low one, 0 or of the other sign, it is a NaN or another)
+        v = fabsf(v) < INFINITY ? v + low : v;
+        if (FT == 8) v += __shfl_xor(v, 40);  // the halves of the steps: rows and columns 8 further
         if (mine) s_sum[wave][pair / k][4 * kf + f] += w * (v * scale[f]);
         acc[f] = 0.f;
       }

@@ -430,3 +430,35 @@ def test_few_host_checks():
         assert lib.moe_lora_few_workspace_size(ctypes.byref(d), 2) == 0
     empty = ml.Dims(0, 256, 384, 8, 3, 16)
     assert call(empty, **{n: None for n in (*names, "y", "work")}) == ml.OK
+
+
+def _infinite(shape, name):
+    """Infinities of both signs in one expert's or one adapter's weights: the formula's results, with their signs."""
+    T, h, I, E, k, nA, r = shape
+    s, logits = _make(*shape, seed=23, none=0.0)
+    ids, w = _choice(logits, k)
+    w = w.float()
+    ids[0, 0], s["adapter_ids"][0] = 1, 0
+    t = s[name] = s[name].clone()
+    t = t[1] if name[0] == "W" else t[0, 1]
+    t[5, 7], t[3, 2], t[6, 0], t[6, 1] = math.inf, -math.inf, math.inf, -math.inf
+    y = ml.forward_few(**s, topk_ids=ids, topk_w=w)
+    ref, bound = _reference(s, ids, w)
+    fin = torch.isfinite(ref)
+    got, want = y.double()[~fin], ref[~fin]
+    assert got.numel() and ((got == want) | (torch.isnan(got) & torch.isnan(want))).all()
+    assert torch.isfinite(y[fin]).all() and ((y.double() - ref).abs() <= bound)[fin].all()
+    return s, ids, w, fin, want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 256, 384, 4, 2, 2, 16), (12, 256, 384, 4, 2, 4, 16), (16, 384, 128, 2, 2, 3, 8),
+                                   (6, 4096, 256, 4, 2, 3, 32), (16, 4096, 128, 2, 1, 2, 16)], ids=str)
+@pytest.mark.parametrize("name", ["W1", "W2", "A1", "B1", "A2"])
+def test_few_infinite_weights(shape, name):
+    """8 and 16 features a workgroup, experts of one token and of many; for W2 the layer's results too."""
+    s, ids, w, fin, want = _infinite(shape, name)
+    if name == "W2":
+        order = [s[n] for n in ("W1", "W2", "A1", "B1", "A2", "B2")]
+        layer = ml.forward_topk(s["x"], ids, w, *order, s["adapter_ids"])[~fin].double()
+        assert ((layer == want) | (torch.isnan(layer) & torch.isnan(want))).all()
