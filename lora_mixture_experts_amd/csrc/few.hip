@@ -505,19 +505,21 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
   load_act(i0);
 
   // The adapters' term: a pair on 16 lanes, four pairs a wavefront at once; of few pairs several lane groups take
-  // some tiles' parts each (the term is linear in z2). A lane adds every step-th tile's part of four ranks, the
-  // lanes of a rank meet, then each lane has a feature (FT = 8: half of its ranks).
+  // some tiles' parts each (the term is linear in z2, where B2 is finite). A lane adds every step-th tile's part of
+  // four ranks, the lanes of a rank meet, then each lane has a feature (FT = 8: half of its ranks).
+  const int slots = 4 * NW;
+  int shares = 1;
+  while (shares * 2 * P <= slots) shares *= 2;
+  uint64_t late = 0;  // lanes whose term is not finite and whose z2 comes in parts
   {
-    const int slots = 4 * NW, quarter = lane >> 4;
-    int shares = 1;
-    while (shares * 2 * P <= slots) shares *= 2;
+    const int quarter = lane >> 4;
     const int per = r / 4, step = 16 / per, at = m / per, q4 = (m - at * per) * 4;
     const int n = m % FT, half = m / FT, nb = FT == 8 ? 2 : 1;
     for (int w0 = 0; w0 < P * shares; w0 += slots) {
       const int w = w0 + quarter * NW + wave;
       const bool in = w < P * shares;
       const int p = in ? w / shares : 0, share = w - p * shares, tok = p / k, e = s_ids[p];
-      const bool on = in && e >= 0 && s_ad[tok] >= 0;
+      bool on = in && e >= 0 && s_ad[tok] >= 0;
       const uint16_t* const b = a.B2 + (((int64_t)s_ad[tok] * a.E + e) * h + n0 + n) * r;
       u32x4 bv[4];
 #pragma unroll
@@ -547,6 +549,11 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
         s += dot8(bq, &s_z[wave][quarter][q0]);
       }
       if (FT == 8) s += __shfl_xor(s, 8);
+      if (shares > 1) {  // (then all pairs are at work at once)
+        const bool defer = on && !(fabsf(s) < INFINITY);
+        late = __ballot(defer);
+        on = on && !defer;
+      }
       // (pairs of one token among the four: one after another)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -613,6 +620,34 @@ __global__ __launch_bounds__(64 * kFewDownWaves) void few_down_kernel(FewArgs a)
       __builtin_amdgcn_sched_barrier(0);
       compute(set[q], i + q);
       __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (late) {
+    // The term of those lanes. Where a feature's row of B2 has infinities or NaNs its pair's first lane group takes
+    // every part of z2: an infinity meets their sum, not the parts, whose signs differ. (Behind the main loop,
+    // where its registers are free.)
+    const int lane16 = threadIdx.x & 15, n = lane16 % FT;
+    const int w = ((threadIdx.x & 63) >> 4) * NW + wave, p = min(w / shares, P - 1), share = w - p * shares;
+    const bool on = (late >> (threadIdx.x & 63)) & 1u;
+    float s = 0.f;
+    if (on) {
+      const uint16_t* const b = a.B2 + (((int64_t)s_ad[p / k] * a.E + s_ids[p]) * h + n0 + n) * r;
+      const float* const parts = a.zpart + (int64_t)s_first[p] * a.tiles * r;
+      bool whole = false;
+      for (int q = 0; q < r; ++q) whole |= (b[q] & 0x7f80) == 0x7f80;
+      const int first = whole ? 0 : a.tiles * share / shares;
+      const int last = whole ? (share == 0 ? a.tiles : 0) : a.tiles * (share + 1) / shares;
+#pragma unroll 1
+      for (int q = 0; q < r && first < last; ++q) {
+        float z = 0.f;
+        for (int i = first; i < last; ++i) z += parts[(int64_t)i * r + q];
+        s += z * bf16_to_f32(b[q]);
+      }
+    }
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      if (((threadIdx.x & 63) >> 4) == q && on && lane16 < FT) s_sum[wave][p / k][n] += s_w[p] * s;
+      __builtin_amdgcn_wave_barrier();
     }
   }
   __syncthreads();

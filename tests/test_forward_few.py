@@ -462,3 +462,12 @@ def test_few_infinite_weights(shape, name):
         order = [s[n] for n in ("W1", "W2", "A1", "B1", "A2", "B2")]
         layer = ml.forward_topk(s["x"], ids, w, *order, s["adapter_ids"])[~fin].double()
         assert ((layer == want) | (torch.isnan(layer) & torch.isnan(want))).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 256, 384, 4, 2, 2, 8), (1, 2048, 1408, 2, 1, 3, 32), (12, 256, 384, 4, 2, 4, 16),
+                                   (16, 384, 128, 2, 2, 3, 8), (16, 128, 128, 8, 8, 2, 64), (6, 4096, 256, 4, 2, 3, 32),
+                                   (3, 4096, 640, 2, 2, 2, 64), (16, 4096, 128, 2, 1, 2, 16)], ids=str)
+def test_few_infinite_second_expand(shape):
+    """z2 of few pairs comes in parts that several lane groups take: their sum meets an infinity of B2, not they."""
+    _infinite(shape, "B2")
