@@ -401,7 +401,7 @@ int moe_lora_linear_lora_plan(const moe_lora_linear_lora_dims *d, moe_lora_linea
 /* The projection above. A bf16 [n_adapters][rank][in_features] and B bf16 [n_adapters][W's rows][rank],
  * dense and 16-byte aligned; adapter_ids int32 [T], in [-1, n_adapters): an id outside acts as -1 and sets
  * MOELORA_FLAG_ADAPTER_RANGE (moe_lora_debug_status on this workspace). An adapter's infinities and NaNs
- * reach the tokens that carry it and no others. Everything else (x, W, w_scale, bias, residual, y over the
+ * reach the tokens that carry it, as the formula has them, and no others. Everything else (x, W, w_scale, bias, residual, y over the
  * residual, errors) as in moe_lora_linear. */
 int moe_lora_linear_lora(const void *x, const void *W, const float *w_scale, const void *bias,
                          const void *residual, const void *A, const void *B, const int32_t *adapter_ids,
@@ -458,7 +458,8 @@ size_t moe_lora_few_workspace_size(const moe_lora_dims *d, int32_t topk);
  * between the two products keep some 16 bits (moe_lora_forward rounds them to bf16), so the results agree
  * with moe_lora_forward's up to that rounding. W1_scale and W2_scale NULL: bf16 W1 and W2; both given:
  * E4M3 codes and scales, as in moe_lora_forward_fp8. Layouts, supported sizes (but T), flags and errors as
- * there; an expert's and an adapter's infinities and NaNs reach the tokens that chose them and no others.
+ * there; an expert's and an adapter's infinities and NaNs reach the tokens that chose them, as the formula
+ * has them, and no others.
  * Pointers 16-byte aligned (scales, router_logits, topk_ids, topk_w and adapter_ids to 4 bytes). Results do
  * not depend on timing. */
 int moe_lora_forward_few(const void *x, const float *router_logits, const int32_t *topk_ids,

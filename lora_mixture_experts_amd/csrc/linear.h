@@ -139,6 +139,28 @@ __device__ __forceinline__ void split_operands(f32x4 v0, f32x4 v1, u32x4& high, 
   low = u32x4{l[0], l[1], l[2], l[3]};
 }
 
+// The largest magnitudes of the two halves' bf16 so far; 0x7f80 and above: infinity or NaN.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void largest(u16x2& m, u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 x = __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu);
+    m = u16x2{m[0] > x[0] ? m[0] : x[0], m[1] > x[1] ? m[1] : x[1]};
+  }
+}
+__device__ __forceinline__ bool all_finite(u16x2 m) { return __ballot(m[0] >= 0x7f80 || m[1] >= 0x7f80) == 0; }
+
+// Eight bf16 with zeros for infinities and NaNs: what low parts are multiplied by. An infinity belongs to the high
+// part's product; times a low part, which may be 0 or of the other sign, it would make the sum a NaN.
+__device__ __forceinline__ u32x4 finite_only(u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
+  }
+  return v;
+}
+
 // Eight values of z: its S splits, added in their order.
 template <int S>
 __device__ __forceinline__ void z_sum(f32x4 (&v)[2], const float* z, int64_t split) {

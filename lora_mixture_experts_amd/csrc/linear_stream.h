@@ -33,7 +33,7 @@ constexpr int kStreamWaves = 8;
 // LORA adds each token's adapter term z B_a^T (z from the shrink's launch). Its items, the adapters of 32
 // tokens (TokenAdapters), are dealt to the wavefronts. An item is a product of its own: rows n0.. of B_a by
 // z of 16 tokens, of which only those that carry the adapter take their sums, so that an adapter's
-// infinities and NaNs stay with its tokens. Beside the first weights' latency it costs little: the 4 us that 4096 x
+// infinities and NaNs stay with its tokens; z's low parts meet B's finite elements only. Beside the first weights' latency it costs little: the 4 us that 4096 x
 // 4096 takes longer for one token with an adapter are the shrink's launch.
 //
 // NT: 16-row token tiles.
@@ -148,6 +148,15 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 #pragma unroll
           for (int h = 0; h < NH; ++h)
             bv[h] = in && n0 + m < a.N ? ldg16(Ba + ((int64_t)h * a.N + n0 + m) * r + rank) : u32x4{0u, 0u, 0u, 0u};
+          if (c + 32 > r) {  // (low parts among the columns)
+            u16x2 most = {0, 0};
+#pragma unroll
+            for (int h = 0; h < NH; ++h) largest(most, bv[h]);
+            if (!all_finite(most) && low) {
+#pragma unroll
+              for (int h = 0; h < NH; ++h) bv[h] = finite_only(bv[h]);
+            }
+          }
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             u32x4 zh, zl;

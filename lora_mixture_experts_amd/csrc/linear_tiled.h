@@ -61,22 +61,11 @@ __device__ __forceinline__ void add_term(f32x16& acc, const f32x16& term, uint32
   for (int v = 0; v < 16; ++v) acc[v] += (mine >> (8 * (v / 4) + v % 4)) & 1u ? term[v] : 0.f;
 }
 
-// The largest magnitudes of the two halves' bf16 so far; 0x7f80 and above: infinity or NaN.
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void largest(u16x2& m, u32x4 v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u16x2 x = __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu);
-    m = u16x2{m[0] > x[0] ? m[0] : x[0], m[1] > x[1] ? m[1] : x[1]};
-  }
-}
-__device__ __forceinline__ bool all_finite(u16x2 m) { return __ballot(m[0] >= 0x7f80 || m[1] >= 0x7f80) == 0; }
-
 // Adapters' terms of the 32 token rows of a wavefront with one row of FN fragments: for each adapter among them
 // (those of index part, part + parts, ..), rows wrow[j] of B_a by z of the tokens that carry it, zeros for the
 // others. Where B has infinities or NaNs, zeros would not keep them off the others: then the product is one of
 // its own, added to the tokens that carry the adapter (as every adapter's, that took 4 us more of 256 tokens of 64
-// adapters, 4096 x 4096: 64 selects for two products).
+// adapters, 4096 x 4096: 64 selects for two products), and z's low parts meet B's finite elements only.
 // B comes straight from global memory into registers, eight operands at a time, and the first eight are
 // loaded while the main loop's first tiles are on their way: one adapter after another behind the main loop
 // took 256 tokens of 64 adapters, 4096 x 4096, 36.8 us; 16 operands in flight 25.0.
@@ -153,7 +142,7 @@ struct AdapterRows {
         u16x2 most = {0, 0};
 #pragma unroll
         for (int j = 0; j < FN * NB; ++j) largest(most, b[d * FN * NB + j]);
-        if (all_finite(most) || who == 0xffffffffu) {
+        if (all_finite(most)) {
           const bool mine = (who >> (lane & 31)) & 1u;
 #pragma unroll
           for (int c = 0; c < 2 * NB; ++c) {
@@ -168,7 +157,10 @@ struct AdapterRows {
 #pragma unroll
             for (int v = 0; v < 16; ++v) term[v] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2 * NB; ++c) term = mfma32(z[c], b[(d * FN + j) * NB + c / 2], term);
+            for (int c = 0; c < 2 * NB; ++c) {
+              const u32x4 bv = b[(d * FN + j) * NB + c / 2];
+              term = mfma32(z[c], c % 2 || (a.r == 8 && lane >= 32) ? finite_only(bv) : bv, term);
+            }
             add_term(acc[j], term, who, lane >> 5);
           }
         }
@@ -298,19 +290,16 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
     auto z_frag = [&](int f, int c, int part) {
       return *reinterpret_cast<const u32x4*>(z_at(wrow0 + f * 32 + fr, r == 8 ? fg : part * bc + 2 * c + fg));
     };
+    u16x2 most = {0, 0};
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) largest(most, b_frag(j, c));
+    const bool finite = all_finite(most);  // zeros of z keep the adapter off the tokens without it
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       if (now[f] == 0u) continue;
-      bool plain = now[f] == 0xffffffffu;  // zeros of z keep the adapter off the tokens without it
-      if (!plain) {
-        u16x2 most = {0, 0};
-#pragma unroll 1
-        for (int c = 0; c < nc; ++c)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) largest(most, b_frag(j, c));
-        plain = all_finite(most);
-      }
-      if (plain) {
+      if (finite) {
         const bool mine = (now[f] >> fr) & 1u;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -331,8 +320,9 @@ __device__ __forceinline__ void add_adapters_tile(f32x16 (&acc)[FM][FN], const L
           for (int v = 0; v < 16; ++v) term[v] = 0.f;
 #pragma unroll 1
           for (int c = 0; c < nc; ++c) {
-            term = mfma32(z_frag(f, c, 0), b_frag(j, c), term);
-            if (r > 8) term = mfma32(z_frag(f, c, 1), b_frag(j, c), term);
+            const u32x4 b = b_frag(j, c), bf = finite_only(b);
+            term = mfma32(z_frag(f, c, 0), r == 8 && fg ? bf : b, term);
+            if (r > 8) term = mfma32(z_frag(f, c, 1), bf, term);
           }
           add_term(acc[f][j], term, now[f], fg);
         }

@@ -441,3 +441,57 @@ def test_linear_lora_host_checks():
         ml.linear_lora(None, None, None, None, None, act="tanh")
     with pytest.raises(ml.MoeLoraError):
         ml.linear_lora_plan(4, 64, 32, 2, 12)
+
+
+def _compare_broken(y, ref, bound):
+    """Finite elements within the bound; infinities and NaNs where the formula has them, with their signs."""
+    fin = torch.isfinite(ref)
+    got, want = y.double()[~fin], ref[~fin]
+    assert ((got == want) | (torch.isnan(got) & torch.isnan(want))).all(), \
+        f"{int((got != want).sum() - (torch.isnan(got) & torch.isnan(want)).sum())} of {got.numel()}"
+    assert torch.isfinite(y[fin]).all() and ((y.double() - ref).abs() <= bound)[fin].all()
+
+
+def _broken_adapters(T, K, N, act, w, r, pattern):
+    """An infinity in one adapter's A, infinities of both signs in another's B: the formula's results, and the same
+    bits for every token without them."""
+    print("linear_lora broken", T, K, N, act, w, r, pattern, flush=True)
+    x, W, scale, _, res = _inputs(T, K, N, act, w, T + N + r, False, True)
+    rows = W.shape[0]
+    A, B = _adapters(3, r, K, rows, r)
+    ids = _ids(T, 3, pattern, 3)
+    want = ml.linear_lora(x, W, A, B, ids, w_scale=scale, act=act, residual=res)
+    A[1, r // 2, 7] = math.inf
+    B[2, min(5, rows - 1), 1] = math.inf
+    B[2, rows // 2, r - 1] = -math.inf
+    B[2, rows - 1, 0], B[2, rows - 1, 5] = math.inf, -math.inf
+    y = ml.linear_lora(x, W, A, B, ids, w_scale=scale, act=act, residual=res)
+    torch.cuda.synchronize()
+    keep = (ids != 1) & (ids != 2)
+    assert torch.equal(y[keep], want[keep])
+    ref, bound = _reference(x, W, scale, None, act, res, A, B, ids)
+    assert not torch.isfinite(ref[ids == 1]).any() and not torch.isfinite(ref[ids == 2][:, -1]).any()
+    _compare_broken(y, ref, bound)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N", [(1, 256, 40), (1, 8192, 40), (2, 256, 64), (17, 272, 33), (30, 256, 64), (40, 512, 2000),
+                                   (48, 272, 1040)])
+@pytest.mark.parametrize("act,w", [("none", "bf16"), ("swiglu", "bf16"), ("none", "e4m3")])
+@pytest.mark.parametrize("r,pattern", [(8, "random"), (8, "one"), (16, "one"), (32, "random"), (64, "distinct")])
+def test_linear_lora_infinite_adapters_of_few_tokens(T, K, N, act, w, r, pattern):
+    """One token in one launch and in two; weights streamed for 16, 32 and 64 tokens, and small tiles."""
+    assert ml.linear_lora_plan(T, K, N, 3, r, act, w == "e4m3")["streamed"] or (K, act) in ((8192, "none"), (8192, "swiglu"), (256, "swiglu"))
+    _broken_adapters(T, K, N, act, w, r, pattern)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r,pattern", [(8, "random"), (16, "one"), (32, "runs"), (64, "random")])
+@pytest.mark.parametrize("act,w", [("none", "bf16"), ("swiglu", "bf16"), ("none", "e4m3")])
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_linear_lora_infinite_adapters_of_every_form(form, act, w, r, pattern):
+    """Every tile, with and without splits: groups of 32 tokens with one adapter, with some, and with none."""
+    T, K, N, rows, cols, split = (SWIGLU_FORMS if act == "swiglu" else FORMS)[form]
+    p = ml.linear_lora_plan(T, K, N, 3, r, act, w == "e4m3")
+    assert (p["streamed"], p["tile_rows"], p["tile_cols"], p["splits"] > 1) == (0, rows, cols, split)
+    _broken_adapters(T, K, N, act, w, r, pattern)
