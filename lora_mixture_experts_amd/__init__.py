@@ -537,9 +537,9 @@ def block_norm(y, residual, weight=None, *, bias=None, post_weight=None, post_bi
     out = the norm of total (before its rounding) with weight [h].
 
     norm: "rms" or "layer", both with an optional bias [h]; gate: None, [T] float32 (through a sigmoid with
-    sigmoid_gate) or [T][h] bf16 (an expanded row is read as one). Without weight out is None; with y None
-    total is residual_scale * residual and only written where it is given. total and out may be y or the
-    residual; an output that shares other bytes with an argument is refused."""
+    sigmoid_gate, which no gate of features takes) or [T][h] bf16 (an expanded row is read as one). Without
+    weight out is None; with y None total is residual_scale * residual and only written where it is given.
+    total and out may be y or the residual; an output that shares other bytes with an argument is refused."""
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {sorted(NORMS)}")
     pair = (_compiled or _native()).block_norm(y, residual, gate, 1 if sigmoid_gate else 0, post_weight, post_bias,

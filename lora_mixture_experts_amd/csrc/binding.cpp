@@ -308,14 +308,15 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.gate = MOELORA_GATE_NONE;
     if (a[2] != Py_None) {
       const Tensor& g = *tensor_of(a[2], "gate");
+      const long sigmoid = PyLong_AsLong(a[3]);
+      if (sigmoid == -1 && PyErr_Occurred()) throw Refused{};
       if (g.dim() == 1) {
         gate = dense(a[2], "gate", at::kFloat, {T}, dev);
-        const long sigmoid = PyLong_AsLong(a[3]);
-        if (sigmoid == -1 && PyErr_Occurred()) throw Refused{};
         d.gate = sigmoid ? MOELORA_GATE_SIGMOID : MOELORA_GATE_TOKEN;
         gate_bytes = bytes_of(g);
       } else {
         check(g, "gate", at::kBFloat16, {T, h}, dev);
+        if (sigmoid) refuse(PyExc_ValueError, "%s: the sigmoid is of a [T] gate%s", "sigmoid_gate");
         if (T > 1 && g.stride(0) == 0) {  // one row for every token
           if (h > 1 && g.stride(1) != 1) refuse(PyExc_ValueError, "%s: the elements of a row must be adjacent%s", "gate");
           gate_bytes = dense_bytes(g.data_ptr(), 2 * h);

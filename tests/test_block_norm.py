@@ -315,3 +315,15 @@ def test_block_norm_host_checks():
     assert call(dims(T=0), y=None, residual=None, w=None, out=None, sum=None) == ml.OK
     with pytest.raises(ValueError):
         ml.block_norm(None, None, norm="batch")
+
+
+@pytest.mark.gpu
+def test_block_norm_refuses_a_sigmoid_of_features():
+    """The sigmoid is of a value a token: a gate of [T][h] would go in as it is."""
+    for gate in ("feature", "element"):
+        s = _inputs(4, 64, False, gate, "rms", 1)
+        for T in (4, 1):
+            one = {n: v[:T] if n in ("y", "residual", "gate") else v for n, v in s.items()}
+            with pytest.raises(ValueError):
+                _call({**one, "sigmoid_gate": True}, "rms")
+            _call(one, "rms")
