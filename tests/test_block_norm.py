@@ -327,3 +327,21 @@ def test_block_norm_refuses_a_sigmoid_of_features():
             with pytest.raises(ValueError):
                 _call({**one, "sigmoid_gate": True}, "rms")
             _call(one, "rms")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,h", [(5, 96), (3, 700), (2, 4096), (2, 20000)])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("size,eps", [(2.0 ** -73, 0.0), (2.0 ** -73, 1e-44), (2.0 ** -66, 1e-38), (2.0 ** -100, 0.0),
+                                      (2.0 ** -41, 0.0), (2.0 ** -45, 1e-28)])
+def test_block_norm_small_rows(T, h, norm, size, eps):
+    """Rows whose squares leave fp32's normal numbers, where eps does not outweigh them: the formula's results, of the
+    block's norm and of the stream's."""
+    s = _inputs(T, h, True, None, norm, 21)
+    s["y"], s["residual"] = (size * s["y"].float()).to(BF), (size * s["residual"].float()).to(BF)
+    s["post_weight"], s["post_bias"] = (size * s["post_weight"].float()).to(BF), None
+    total, out = _call(s, norm, rs=1.0, bs=0.5, eps=eps)
+    # (the call's eps is fp32, which has 7 * 2^-149 = 9.81e-45 for 1e-44: 2% less)
+    want = _expect(s, norm, rs=1.0, bs=0.5, eps=torch.tensor(eps, dtype=torch.float32).item())
+    _within(total, want[0])
+    _within(out, want[1])
