@@ -30,28 +30,43 @@ struct LoraLayout {
   size_t z, groups, part, total;
 };
 
-// The shrink's form: adapter by adapter (slots = 0) for batches, else 32 tokens after another, with four workgroups
-// for their adapters (prompts mostly have one). The first reads an adapter's A once for 16 of its tokens, the
-// second once for every 32 tokens. Measured, first and second (us, 4096 x 1024, rank 16, random ids): 64 tokens of 1
-// adapter 14.3, 14.7; of 8 15.7, 17.5; of 64 17.0, 26.7; 256 of 1 16.3, 16.7; of 64 20.7, 31.1; 512 of 2 23.1, 21.4; of
-// 16 24.8, 32.1; of 64 25.3, 42.7. The first form's parts share the tokens of one adapter, as far as 2048 workgroups go,
-// most of which find no token and leave (101 tokens of one of 43 adapters, 2792 x 660, rank 64: 38.2 with one part, 21.4
-// with 1024 workgroups, 19.6).
-// K is split (not below 512 of it) where that leaves CUs idle.
+// The shrink's form: adapter by adapter (slots = 0) for batches, else 32 tokens after another with `slots` workgroups
+// for their adapters (one each up to 32; four for prompts, which mostly have one). The first reads an adapter's A once
+// for 16 of its tokens and costs a workgroup an adapter that the call knows, carried or not; the second reads A once
+// for every 32 tokens. Both launches together, first and second form at their best splits (us on the device, 4096 x
+// 4096, random ids): rank 64, 64 adapters, 2 tokens 17.1 17.2, 8 22.2 22.4, 32 27.8 29.7, 128 39.8 41.5, 512 64 92; 256
+// adapters 18.1 17.4, 22.8 22.6, 30.1 30.8, 45.6 42.9, 86 107; 1024 adapters 21.3 17.3, 26.3 22.8, 32.6 30.8, 51.6
+// 43.9, 128 121; rank 16, 64 adapters 11.9 12.1, 14.2 14.8, 19.1 21.6, 24.4 27.6, 37 46; 1024 13.1 12.1, 15.8 14.7, 22.9
+// 22.7, 29.7 28.4, 50 49. With K 1024 the first form is the faster one up to 1024 adapters (4096 x 1024, rank 8, 64
+// tokens 20.0 22.8).
+// The first form's parts share the tokens of one adapter, as far as 2048 workgroups go, most of which find no token and
+// leave (101 tokens of one of 43 adapters, 2792 x 660, rank 64: 38.2 with one part, 21.4 with 1024 workgroups, 19.6).
+// K is split (not below 512 of it) where that leaves CUs idle. Every split is z's size more to read for every adapter of
+// the projection's launch, which is why their number falls with the adapters' ranks and rises with K (16 tokens of 64
+// adapters of rank 64, 4096 x 4096: 45.6 with 8, 32.8 with 4, 30.4 with 2; 64 tokens of rank 64, 1024 x 1024: 59.6 with 2, 41.4
+// with 1). On 480 shapes (K 1024 to 8192, 2 to 512 tokens, 1 to 1024 adapters) the choice is 1.6% above the fastest
+// on average, at most 32%.
 struct ShrinkPlan {
   int slots, splits, parts;
 };
 
 ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
   const moe_lora_linear_dims& l = d->linear;
-  const int groups = std::max(1, (l.T + 31) / 32);
+  const int groups = std::max(1, (l.T + 31) / 32), carried = std::max(1, std::min(l.T, d->n_adapters));
   ShrinkPlan p;
-  const bool batch = l.T <= kAdapterShrinkTokens && d->n_adapters <= 1024 && l.T * l.x_stride * 2 < ((int64_t)1 << 31);
-  p.slots = batch ? 0 : std::min({4, std::max(l.T, 1), d->n_adapters});
-  const int busy = batch ? std::max(1, std::min(l.T, d->n_adapters)) : groups, enough = batch ? 257 : 128;
+  const bool prompt = l.T > kAdapterShrinkTokens;
+  const bool by_adapter = !prompt && d->n_adapters <= (l.in_features <= 1024 ? 1024 : l.T > 8 ? 256 : 128) &&
+                          l.T * l.x_stride * 2 < ((int64_t)1 << 31);
+  p.slots = by_adapter ? 0 : std::min(prompt ? 4 : 32, carried);
+  const int busy = prompt ? groups : by_adapter ? carried : groups * p.slots;
+  const int enough = prompt ? 127 : by_adapter ? 128 : 255;
+  const int most = prompt || (carried <= 4 && l.T <= 32)
+                       ? 8
+                       : std::max(1, std::min({8, 256 / d->rank, 2 * l.in_features / (carried * d->rank)}));
   p.splits = 1;
-  while (p.splits < 8 && busy * p.splits < enough && l.in_features >= 1024 * p.splits) p.splits *= 2;
-  p.parts = batch ? std::max(1, std::min((l.T + 15) / 16, 2048 / (d->n_adapters * p.splits))) : 1;
+  while (p.splits < most && busy * p.splits <= enough && l.in_features >= 1024 * p.splits) p.splits *= 2;
+  while (by_adapter && p.splits > 1 && d->n_adapters * p.splits > 1024) p.splits /= 2;
+  p.parts = by_adapter ? std::max(1, std::min((l.T + 15) / 16, 2048 / (d->n_adapters * p.splits))) : 1;
   return p;
 }
 

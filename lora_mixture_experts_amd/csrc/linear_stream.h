@@ -148,7 +148,13 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 #pragma unroll
           for (int h = 0; h < NH; ++h)
             bv[h] = in && n0 + m < a.N ? ldg16(Ba + ((int64_t)h * a.N + n0 + m) * r + rank) : u32x4{0u, 0u, 0u, 0u};
-          if (c + 32 > r) {  // (low parts among the columns)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            u32x4 zh, zl;
+            z_operands(a, in ? 32 * g + 16 * q + m : a.T, rank, zh, zl);
+            zv[q] = low ? zl : zh;
+          }
+          if (c + 32 > r) {  // (low parts among the columns; behind z's loads, which need not wait for B's)
             u16x2 most = {0, 0};
 #pragma unroll
             for (int h = 0; h < NH; ++h) largest(most, bv[h]);
@@ -156,12 +162,6 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 #pragma unroll
               for (int h = 0; h < NH; ++h) bv[h] = finite_only(bv[h]);
             }
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            u32x4 zh, zl;
-            z_operands(a, in ? 32 * g + 16 * q + m : a.T, rank, zh, zl);
-            zv[q] = low ? zl : zh;
           }
 #pragma unroll
           for (int h = 0; h < NH; ++h)

@@ -495,3 +495,14 @@ def test_linear_lora_infinite_adapters_of_every_form(form, act, w, r, pattern):
     p = ml.linear_lora_plan(T, K, N, 3, r, act, w == "e4m3")
     assert (p["streamed"], p["tile_rows"], p["tile_cols"], p["splits"] > 1) == (0, rows, cols, split)
     _broken_adapters(T, K, N, act, w, r, pattern)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 32, 40, 512])
+@pytest.mark.parametrize("nA,K", [(1, 2048), (40, 1024), (300, 4096), (512, 2048), (513, 4096), (1025, 528)])
+@pytest.mark.parametrize("r", [8, 64])
+def test_linear_lora_many_adapters_known(T, nA, K, r):
+    """Few tokens of many adapters, on both sides of the borders between the shrink's forms and their splits."""
+    _check(T, K, 48, "none", "bf16", r, nA, "random")
+    if T > 1:
+        _check(T, K, 48, "none", "bf16", r, nA, "distinct", seed=3)
