@@ -471,3 +471,38 @@ def test_few_infinite_weights(shape, name):
 def test_few_infinite_second_expand(shape):
     """z2 of few pairs comes in parts that several lane groups take: their sum meets an infinity of B2, not they."""
     _infinite(shape, "B2")
+
+
+def _col_tiles(shape):
+    """Column tiles of a workgroup of the first product, from the size of the workspace that z2's parts take."""
+    T, h, I, E, k, nA, r = shape
+    need = ml.lib().moe_lora_few_workspace_size(ctypes.byref(ml.Dims(T, h, I, E, nA, r)), k)
+    P = T * k
+
+    def size(ct, splits):
+        parts = [4 * P] * 4 + [64 * P] * 2 + [4 * P * r * splits, 4 * P * I, 4 * P * r * (I // (16 * ct))]
+        return 256 + sum((n + 255) // 256 * 256 for n in parts)
+
+    return {ct for ct in (1, 2, 4) for splits in (1, 2, 4) if size(ct, splits) == need}
+
+
+FOUR_TILES = [  # some tokens an expert, all of them, one; 8 and 16 features a workgroup of the second product
+    (16, 128, 256, 128, 8, 3, 8), (16, 256, 256, 128, 8, 5, 32), (13, 128, 256, 128, 16, 2, 64), (16, 256, 4096, 8, 2, 5, 32),
+    (16, 128, 32768, 1, 1, 20, 64), (16, 128, 32768, 1, 1, 3, 8), (16, 4096, 1024, 32, 4, 2, 64), (3, 4096, 11008, 3, 2, 2, 8)]
+
+
+def test_few_shapes_of_four_column_tiles():
+    for shape in FOUR_TILES:
+        assert _col_tiles(shape) == {4}, shape
+    assert _col_tiles((1, 1024, 768, 128, 8, 4, 32)) == {2} and _col_tiles((2, 384, 256, 5, 5, 2, 64)) == {1}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", FOUR_TILES, ids=str)
+@pytest.mark.parametrize("w", ["bf16", "e4m3"])
+def test_few_four_column_tiles(shape, w):
+    """The first product's widest form at every rank, with experts of many tokens."""
+    print("forward_few", shape, w, flush=True)
+    s, logits = _make(*shape, w, seed=29)
+    y = ml.forward_few(**s, router_logits=logits, topk=shape[4])
+    _compare(y, _reference(s, *_choice(logits, shape[4])))
