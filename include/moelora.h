@@ -390,9 +390,9 @@ typedef struct {
   int32_t rank;       /* 8, 16, 32 or 64 */
 } moe_lora_linear_lora_dims;
 
-/* Bytes of device workspace moe_lora_linear_lora needs (0 for sizes that are not supported): z, the
- * adapters of every 32 tokens, the sums of a split reduction. 256-byte aligned, no initialisation needed.
- * Host-only. */
+/* Bytes of device workspace moe_lora_linear_lora needs (0 for sizes out of the ranges above): z, the
+ * adapters of every 32 tokens, the sums of a split reduction. More tokens may need less: one workspace for
+ * several sizes has the largest of theirs. 256-byte aligned, no initialisation needed. Host-only. */
 size_t moe_lora_linear_lora_workspace_size(const moe_lora_linear_lora_dims *d);
 
 /* moe_lora_linear_plan for moe_lora_linear_lora. Host-only. */
@@ -401,7 +401,8 @@ int moe_lora_linear_lora_plan(const moe_lora_linear_lora_dims *d, moe_lora_linea
 /* The projection above. A bf16 [n_adapters][rank][in_features] and B bf16 [n_adapters][W's rows][rank],
  * dense and 16-byte aligned; adapter_ids int32 [T], in [-1, n_adapters): an id outside acts as -1 and sets
  * MOELORA_FLAG_ADAPTER_RANGE (moe_lora_debug_status on this workspace). An adapter's infinities and NaNs
- * reach the tokens that carry it, as the formula has them, and no others. Everything else (x, W, w_scale, bias, residual, y over the
+ * reach the tokens that carry it, as the formula has them, and no others (w_scale, finite, multiplies the
+ * parts of a split sum). Everything else (x, W, w_scale, bias, residual, y over the
  * residual, errors) as in moe_lora_linear. */
 int moe_lora_linear_lora(const void *x, const void *W, const float *w_scale, const void *bias,
                          const void *residual, const void *A, const void *B, const int32_t *adapter_ids,
@@ -447,7 +448,7 @@ int moe_lora_block_norm(const void *y, const void *residual, const void *gate, c
                         const moe_lora_block_norm_dims *d, void *sum, void *out, void *stream);
 
 /* Bytes of device workspace moe_lora_forward_few needs (0 for sizes that are not supported): the choices,
- * the shrink outputs and the activations. 256-byte aligned, no initialisation needed. Host-only. */
+ * the shrink outputs and the activations. More tokens may need less, as above. 256-byte aligned, no initialisation needed. Host-only. */
 size_t moe_lora_few_workspace_size(const moe_lora_dims *d, int32_t topk);
 
 /* The layer for a few tokens, as a decode step of one or a few requests calls it (page "AWS SageMaker MoE
@@ -456,7 +457,7 @@ size_t moe_lora_few_workspace_size(const moe_lora_dims *d, int32_t topk);
  * topk_ids and topk_w NULL) or of moe_lora_forward_topk (topk_ids int32 and topk_w f32 [T][topk] given,
  * router_logits NULL), for T in [0, 16], in three launches and without a sorted layout. The activations
  * between the two products keep some 16 bits (moe_lora_forward rounds them to bf16), so the results agree
- * with moe_lora_forward's up to that rounding. W1_scale and W2_scale NULL: bf16 W1 and W2; both given:
+ * with moe_lora_forward's up to that rounding (finite weights). W1_scale and W2_scale NULL: bf16 W1 and W2; both given:
  * E4M3 codes and scales, as in moe_lora_forward_fp8. Layouts, supported sizes (but T), flags and errors as
  * there; an expert's and an adapter's infinities and NaNs reach the tokens that chose them, as the formula
  * has them, and no others.

@@ -71,10 +71,11 @@ ShrinkPlan plan_shrink(const moe_lora_linear_lora_dims* d) {
 }
 
 // One token in one launch, where the streaming kernel takes it and forming z in every workgroup costs less than the
-// launch that it saves (some 4 us): its loads of A are K r a round of 256 workgroups. Two launches against one
-// (us), by that number: 16384 (1024 x 1024, rank 16) 7.2, 4.4; 65536 (4096 x 4096, rank 16) 12.1, 10.8; (1024 x
-// 1024, rank 64) 11.2, 7.7; (8192 x 1024 E4M3, rank 8) 11.2, 11.8; 131072 (4096 x 4096, rank 32) 13.2, 14.4; (2048
-// x 2048, rank 64) 12.6, 12.5; (8192 x 1024 E4M3, rank 16) 11.6, 14.8.
+// launch that it saves (some 3 us): its loads of A are K r a round of 256 workgroups. Two launches against one
+// (us on the device, inputs x outputs), by that number: 16384 (1024 x 1024, rank 16) 7.2, 4.5; 32768 (4096 x 1024,
+// rank 8) 9.9, 9.0; 65536 (4096 x 4096, rank 16) 11.3, 10.9; (1024 x 1024, rank 64) 11.3, 7.8; (4096 x 1024, rank 16)
+// 10.1, 10.4; (8192 x 1024 E4M3, rank 8) 11.2, 12.0; 131072 (4096 x 4096, rank 32) 12.7, 14.7; (1024 x 8192, rank 64)
+// 15.6, 13.6; (8192 x 1024 E4M3, rank 16) 11.5, 14.9. Of 124 shapes, 11 on the slower side, by at most 2.6 us.
 bool one_launch(const moe_lora_linear_lora_dims* d, const LinearPlan& p) {
   const moe_lora_linear_dims& l = d->linear;
   const int64_t rounds = ((int64_t)l.out_features + 4095) / 4096;  // of workgroups, 16 columns each

@@ -15,7 +15,10 @@
 // With up to 16 tokens the tokens of an expert are columns of a 16x16x32 MFMA whose rows are its weights'. An
 // expert's and an adapter's sums go to the tokens that chose them, so that nothing of theirs reaches others. No
 // pair is sorted: an expert is computed by the workgroup of the first pair that names it. Bound by the bytes
-// of the experts' weights, for one token and small experts by the latency of the three launches. Measured, the
+// of the experts' weights, for one token and small experts by the latency of the three launches, for many tokens on few
+// experts by what few_down's workgroups load besides: W2's rows again for every 8 tokens of an expert (4 in the form of
+// 8 features), and each of them act and z2's parts, P I 4 and P r I / (4 CT) bytes (12 tokens, one expert of 2048 x
+// 5504, rank 64: 7.6 + 29.4 + 35.7 us for 85 MB). Measured, the
 // caches empty: 1 token, 2 of 16 experts of 4096 x 11008, 5.2 + 72.6 + 43.7 us (5.0 and 4.1 TB/s of the two
 // products' weights); 1 token, 8 of 128 of 2048 x 768, 6.7 + 14.5 + 14.6; 16 tokens of those, 85 experts chosen,
 // 9.6 + 119 + 58.1 (4.5 and 4.6 TB/s).

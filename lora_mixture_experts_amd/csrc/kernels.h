@@ -177,7 +177,7 @@ struct TokenAdapters {
   uint32_t tokens[32];  // bit i: token i of the 32
 };
 
-constexpr int kAdapterShrinkTokens = 512;  // tokens of a batch whose shrink goes adapter by adapter
+constexpr int kAdapterShrinkTokens = 512;  // the most tokens of a batch (its shrink may go adapter by adapter)
 // LoRA shrink of tokens in their own order: z = x A_a^T for the projection with adapters, and the
 // adapters of every 32 tokens.
 struct TokenShrinkArgs {

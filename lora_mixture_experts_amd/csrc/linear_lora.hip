@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void token_shrink_kernel(TokenSh
 
 // Shrink of batches, whose tokens are mostly of different requests: a workgroup an adapter (blockIdx.y) and split
 // of K, which looks its tokens up among all ids, so that A is read once for 16 of them: 256 tokens of 4096, 64
-// adapters of rank 16, 6.3 us (by 32 tokens as above, which reads it three times, 10.5). The tokens of one adapter, 16
+// adapters of rank 16, 5.9 us (by 32 tokens as above, which reads it three times, 10.5). The tokens of one adapter, 16
 // after 16, are shared by blockIdx.z. The workgroups behind the last adapter write the tokens' groups.
 template <int NQ>
 __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(TokenShrinkArgs a) {
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Token
 // One token, in one launch: the streaming kernel (16 output columns a workgroup, the 64-wide K chunks dealt to its 8
 // wavefronts), in which every workgroup forms the token's z for itself: the adapter's rows of A are NQ more tiles
 // of 16 rows by the same x, read by all workgroups and so from the caches. All columns of a product are the
-// token. z stays fp32. 4096 x 4096, rank 16: 10.8 us for 8.3 of the product alone and 12.1 in two launches; 512 x 512
-// 3.8 for 6.9.
+// token. z stays fp32. 4096 x 4096, rank 16: 10.9 us for 8.3 of the product alone and 11.3 in two launches (E4M3 9.2
+// for 9.5); 512 inputs, 4096 outputs 4.1 for 6.9.
 template <int NQ, bool GATED, bool W8>
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_lora_one_kernel(LinearArgs a, TokenShrinkArgs sh) {
   constexpr int WK = kStreamWaves, NH = GATED ? 2 : 1, WL = W8 ? 1 : 2, WB = W8 ? 1 : 2, KJ = W8 ? 8 : 32;

@@ -33,8 +33,9 @@ constexpr int kStreamWaves = 8;
 // LORA adds each token's adapter term z B_a^T (z from the shrink's launch). Its items, the adapters of 32
 // tokens (TokenAdapters), are dealt to the wavefronts. An item is a product of its own: rows n0.. of B_a by
 // z of 16 tokens, of which only those that carry the adapter take their sums, so that an adapter's
-// infinities and NaNs stay with its tokens; z's low parts meet B's finite elements only. Beside the first weights' latency it costs little: the 4 us that 4096 x
-// 4096 takes longer for one token with an adapter are the shrink's launch.
+// infinities and NaNs stay with its tokens; z's low parts meet B's finite elements only. 16 tokens of 8 adapters of
+// rank 16, 4096 x 4096: 15.3 us on the device for 9.8 without adapters, the shrink's launch the most of it. (One
+// token mostly takes linear_lora_one_kernel.)
 //
 // NT: 16-row token tiles.
 // A load at or past the end of its row (K is a multiple of 8, not of 64) or of a row past the end

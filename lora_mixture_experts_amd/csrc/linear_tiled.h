@@ -178,9 +178,10 @@ struct AdapterRows {
 // LDS once the main loop is done: z of the tile's rows as operands, and the rows of B of one adapter of the tile
 // after another, straight into one of two buffers while the adapter before is multiplied. 16-byte chunks,
 // XOR-swizzled by the row so that fragment reads are free of bank conflicts. (With B in registers as above the
-// accumulators spilled: 4096 x 28672 x 4096, rank 64, 1.60 ms; so 854 us, 787 without adapters: 13 us of a tile's
-// 144, and 28 of shrink.) wrow_of(i): B's row of row i of the weight tile,
-// -1 past the end; groups: the adapters of the tile's rows, in LDS (loaded beside the main loop's first tiles: a
+// accumulators spilled: 4096 x 28672 x 4096, rank 64, 1.60 ms; so 837 to 900 us by the card, 787 without adapters: 13
+// us of a tile's 144, and 28 of shrink.) A wavefront looks an adapter's rows through for infinities once, for all its
+// tokens (512 adapters of rank 16 at random over 2048 tokens: 1913 us with a look for every 32, 1657). wrow_of(i): B's
+// row of row i of the weight tile, -1 past the end; groups: the adapters of the tile's rows, in LDS (loaded beside the main loop's first tiles: a
 // load behind the main loop is the longer the more the other workgroups load). Every wavefront of the workgroup
 // calls it.
 template <int BM, int BN, int NWV, int FM, int FN, class Row>

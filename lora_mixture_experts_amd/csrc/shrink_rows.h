@@ -2,8 +2,8 @@
 // adapter. Internal to libmoelora.
 //
 // 16x16x32 MFMAs with the rows of A on their A side and 16 tokens on their B side. The wavefronts take the
-// 64-wide K chunks in turn, two to four in flight each, and their sums meet in LDS, where the caller adds them in
-// wavefront order: fp32, in an order that does not depend on timing.
+// 64-wide K chunks in turn, the next one in flight during a chunk's products, and their sums meet in LDS, where
+// the caller adds them in wavefront order: fp32, in an order that does not depend on timing.
 #pragma once
 
 #include "common.h"
